@@ -26,6 +26,7 @@ P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int32
 INT = ctypes.c_int
+F32 = ctypes.c_float
 
 BSQ_OK, BSQ_ERR_INVALID_ARG, BSQ_ERR_UNSUPPORTED, BSQ_ERR_WORKSPACE_TOO_SMALL, BSQ_ERR_HIP = range(5)
 BSQ_BF16, BSQ_F32 = 0, 1
@@ -48,6 +49,15 @@ _SIGS = {
     "bsq_grouped_gemm_fwd_mxfp8": ([P, P, P, P, P, I32, I64, I64, I64, P, INT, P, ctypes.c_size_t, P], INT),
     "bsq_grouped_gemm_bf16": ([P, P, P, I32, I64, I64, I64, P, INT, P, ctypes.c_size_t, P], INT),
     "bsq_grouped_gemm_w4a16": ([P, P, P, P, P, I32, I64, I64, I64, P, INT, P, ctypes.c_size_t, P], INT),
+    "bsq_moe_route": ([P, INT, I64, I32, I64, I32, P, P, I32, F32, F32, P, P, P, P, P, P, ctypes.c_size_t, P], INT),
+    "bsq_moe_route_workspace_size": ([I64, I32], ctypes.c_size_t),
+    "bsq_moe_route_bwd": ([P, INT, I64, I32, I64, I32, P, P, P, P, P, P, I32, F32, F32, P, I64, P], INT),
+    "bsq_moe_dispatch": ([P, I64, I32, I32, P, P, P, P, ctypes.c_size_t, P], INT),
+    "bsq_moe_dispatch_workspace_size": ([I64, I32, I32], ctypes.c_size_t),
+    "bsq_moe_combine": ([P, INT, I64, I64, I64, P, P, I64, I32, P, I64, P], INT),
+    "bsq_moe_combine_bwd": ([P, INT, I64, I64, I64, P, I64, I64, P, P, I32, P, I32, P, I64, P, P], INT),
+    "bsq_quantize_fp8b128": ([P, I64, I64, I64, P, I64, P, I32, P, P, P, P, P], INT),
+    "bsq_quantize_fp8b128_weights": ([P, I32, I64, I64, I64, P, P, P, P], INT),
     "bsq_workspace_size": ([INT, I32, I64, I64, I64], ctypes.c_size_t),
     "bsq_colwise_padded_cols": ([I32, I64], I64),
     "bsq_status_string": ([INT], ctypes.c_char_p),
@@ -437,6 +447,240 @@ def bsq_grouped_gemm_bwd(offsets, m_total, n, k, dy_q=None, wt_q=None, dyt_q=Non
                                      _ptr(dx), dx_dtype, _ptr(dw), dw_dtype, flags, _ptr(workspace),
                                      workspace.numel() * workspace.element_size(), _stream(stream)))
     return dx, dw
+
+
+def _dtype_id(t, name):
+    _dev(t, name, (torch.bfloat16, torch.float32))
+    return BSQ_F32 if t.dtype == torch.float32 else BSQ_BF16
+
+
+def _shaped(t, name, dtypes, shape, dev):
+    """Checks a dense input or output buffer."""
+    _dev(t, name, dtypes)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} on {dev}")
+    return t
+
+
+def _scratch(need, workspace, dev, stream):
+    if workspace is None:
+        return _empty(stream, (need,), dtype=torch.uint8, device=dev)
+    _dev(workspace, "workspace", (workspace.dtype,))
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {dev}")
+    if workspace.numel() * workspace.element_size() < need:
+        raise ValueError(f"workspace must hold {need} bytes")
+    return workspace
+
+
+def _offsets(offsets, dev):
+    _dev(offsets, "offsets", (torch.int32,))
+    if offsets.dim() != 1 or offsets.numel() < 2 or not offsets.is_contiguous() or offsets.device != dev:
+        raise ValueError(f"offsets must be contiguous [num_experts + 1] on {dev}")
+    return offsets.numel() - 1
+
+
+def bsq_moe_route_workspace_size(tokens, num_experts):
+    return int(_lib.bsq_moe_route_workspace_size(tokens, num_experts))
+
+
+def bsq_moe_dispatch_workspace_size(tokens, top_k, num_experts):
+    return int(_lib.bsq_moe_dispatch_workspace_size(tokens, top_k, num_experts))
+
+
+def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0, loss_coef=0.0, workspace=None,
+                  stream=None):
+    """Top-k routing of ``logits`` [tokens, experts] (bf16 or f32) with the balance loss.
+    bias f32 [experts] is added for the selection only; mask (uint8 or bool) [tokens]
+    is 0 for padding.  Returns (expert_ids i32 [tokens, top_k], weights f32
+    [tokens, top_k], lse f32 [tokens], counts i32 [experts + 1], loss f32 [1]);
+    counts holds the tokens per expert, then the tokens that go anywhere."""
+    dt = _dtype_id(logits, "logits")
+    T, E, ld = _rows_ld(logits)
+    dev = logits.device
+    if bias is not None:
+        _shaped(bias, "bias", (torch.float32,), (E,), dev)
+    if mask is not None:
+        _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
+    ids = _empty(stream, (T, top_k), dtype=torch.int32, device=dev)
+    weights = _empty(stream, (T, top_k), dtype=torch.float32, device=dev)
+    lse = _empty(stream, (T,), dtype=torch.float32, device=dev)
+    counts = _empty(stream, (E + 1,), dtype=torch.int32, device=dev)
+    loss = _empty(stream, (1,), dtype=torch.float32, device=dev)
+    workspace = _scratch(bsq_moe_route_workspace_size(T, E), workspace, dev, stream)
+    _check("bsq_moe_route",
+           _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
+                              scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss),
+                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return ids, weights, lse, counts, loss
+
+
+def bsq_moe_route_bwd(logits, expert_ids, weights, lse, counts, dweights=None, dloss=None, normalize=True, scale=1.0,
+                      loss_coef=0.0, dlogits=None, stream=None):
+    """Gradient of ``logits`` from those of the weights (f32 [tokens, top_k]) and of
+    the loss (f32 [1], on the device); either may be None.  The other arguments are
+    those and the outputs of bsq_moe_route."""
+    dt = _dtype_id(logits, "logits")
+    T, E, ld = _rows_ld(logits)
+    dev = logits.device
+    K = expert_ids.shape[-1]
+    _shaped(expert_ids, "expert_ids", (torch.int32,), (T, K), dev)
+    _shaped(weights, "weights", (torch.float32,), (T, K), dev)
+    _shaped(lse, "lse", (torch.float32,), (T,), dev)
+    _shaped(counts, "counts", (torch.int32,), (E + 1,), dev)
+    if dweights is not None:
+        _shaped(dweights, "dweights", (torch.float32,), (T, K), dev)
+    if dloss is not None:
+        _dev(dloss, "dloss", (torch.float32,))
+        if dloss.numel() != 1 or dloss.device != dev:
+            raise ValueError(f"dloss must hold one value on {dev}")
+    if dlogits is None:
+        dlogits = _empty(stream, (T, E), dtype=logits.dtype, device=dev)
+    _dev(dlogits, "dlogits", (logits.dtype,))
+    if tuple(dlogits.shape) != (T, E) or dlogits.device != dev:
+        raise ValueError(f"dlogits must have shape {(T, E)} on {dev}")
+    ldd = _rows_ld(dlogits)[2]
+    _check("bsq_moe_route_bwd",
+           _lib.bsq_moe_route_bwd(_ptr(logits), dt, T, E, max(ld, E), K, _ptr(expert_ids), _ptr(weights), _ptr(lse),
+                                  _ptr(counts), _ptr(dweights), _ptr(dloss), int(normalize), scale, loss_coef,
+                                  _ptr(dlogits), max(ldd, E), _stream(stream)))
+    return dlogits
+
+
+def bsq_moe_dispatch(expert_ids, num_experts, workspace=None, stream=None):
+    """Expert-sorted order of the choices ``expert_ids`` (i32 [tokens, top_k]; an id
+    outside [0, num_experts) is no choice).  Returns (offsets i32 [num_experts + 1],
+    row_index i32 [tokens * top_k], slot i32 [tokens, top_k])."""
+    _dev(expert_ids, "expert_ids", (torch.int32,))
+    if expert_ids.dim() != 2 or not expert_ids.is_contiguous():
+        raise ValueError("expert_ids must be contiguous [tokens, top_k]")
+    T, K = expert_ids.shape
+    dev = expert_ids.device
+    offsets = _empty(stream, (num_experts + 1,), dtype=torch.int32, device=dev)
+    row_index = _empty(stream, (T * K,), dtype=torch.int32, device=dev)
+    slot = _empty(stream, (T, K), dtype=torch.int32, device=dev)
+    workspace = _scratch(bsq_moe_dispatch_workspace_size(T, K, num_experts), workspace, dev, stream)
+    _check("bsq_moe_dispatch",
+           _lib.bsq_moe_dispatch(_ptr(expert_ids), T, K, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot),
+                                 _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    return offsets, row_index, slot
+
+
+def bsq_moe_combine(ye, slot, weights=None, y=None, stream=None):
+    """y[t] = sum_j weights[t, j] * ye[slot[t, j]] (bf16 or f32 rows; weights None:
+    ones).  Choices whose slot is outside ye add nothing."""
+    dt = _dtype_id(ye, "ye")
+    M, W, ld = _rows_ld(ye)
+    dev = ye.device
+    T, K = slot.shape
+    _shaped(slot, "slot", (torch.int32,), (T, K), dev)
+    if weights is not None:
+        _shaped(weights, "weights", (torch.float32,), (T, K), dev)
+    if y is None:
+        y = _empty(stream, (T, W), dtype=ye.dtype, device=dev)
+    _dev(y, "y", (ye.dtype,))
+    if tuple(y.shape) != (T, W) or y.device != dev:
+        raise ValueError(f"y must have shape {(T, W)} on {dev}")
+    _check("bsq_moe_combine",
+           _lib.bsq_moe_combine(_ptr(ye), dt, M, W, ld, _ptr(slot), _ptr(weights), T, K, _ptr(y), _rows_ld(y)[2],
+                                _stream(stream)))
+    return y
+
+
+def bsq_moe_combine_bwd(dy, ye, slot, weights=None, offsets=None, m_total=None, dye=None, need_dweights=True,
+                        stream=None):
+    """Gradients of bsq_moe_combine: (dye [m_total, width], dweights f32 [tokens, top_k]
+    or None).  With ``offsets`` (of the dispatch) the rows of dye that no choice
+    owns become zero, without they are left as they are.  ye may be None where
+    dweights is not needed; m_total then gives the rows of dye."""
+    dt = _dtype_id(dy, "dy")
+    T, W, ld = _rows_ld(dy)
+    dev = dy.device
+    K = slot.shape[-1]
+    _shaped(slot, "slot", (torch.int32,), (T, K), dev)
+    if weights is not None:
+        _shaped(weights, "weights", (torch.float32,), (T, K), dev)
+    if ye is None and (need_dweights or m_total is None):
+        raise ValueError("without ye, m_total is needed and dweights cannot be computed")
+    M = ye.shape[0] if ye is not None else m_total
+    ldye = 0
+    if ye is not None:
+        _dev(ye, "ye", (dy.dtype,))
+        if ye.dim() != 2 or ye.shape[1] != W or ye.device != dev:
+            raise ValueError(f"ye must have {W} columns on {dev}")
+        ldye = _rows_ld(ye)[2]
+    E = 0 if offsets is None else _offsets(offsets, dev)
+    if dye is None:
+        dye = _empty(stream, (M, W), dtype=dy.dtype, device=dev)
+    _dev(dye, "dye", (dy.dtype,))
+    if tuple(dye.shape) != (M, W) or dye.device != dev:
+        raise ValueError(f"dye must have shape {(M, W)} on {dev}")
+    dw = _empty(stream, (T, K), dtype=torch.float32, device=dev) if need_dweights else None
+    _check("bsq_moe_combine_bwd",
+           _lib.bsq_moe_combine_bwd(_ptr(dy), dt, T, W, ld, _ptr(ye), M, ldye, _ptr(slot), _ptr(weights), K,
+                                    _ptr(offsets), E, _ptr(dye), _rows_ld(dye)[2], _ptr(dw), _stream(stream)))
+    return dye, dw
+
+
+def bsq_quantize_fp8b128(x, row_index=None, offsets=None, rows_form=True, row=None, t=None, stream=None):
+    """FP8B128 of bf16 ``x`` [src_rows, cols], or of x[row_index] (i32; out-of-range
+    indices give zero rows).  Returns (row, t): row = (codes u8 [rows, cols], scale
+    f32 [ceil(cols/128), rows]), or None with rows_form=False; t = the
+    token-column form (t_codes u8 [cols, P], t_scale f32 [P/128, cols]) where
+    ``offsets`` (i32 [groups + 1]) is given, else None."""
+    _dev(x, "x", _BF16)
+    src_rows, cols, ld = _rows_ld(x)
+    dev = x.device
+    rows = src_rows
+    if row_index is not None:
+        rows = row_index.numel()
+        _shaped(row_index, "row_index", (torch.int32,), (rows,), dev)
+    nb = (cols + 127) // 128
+    G = 0
+    if rows_form:
+        codes, scale = row or (_empty(stream, (rows, cols), dtype=torch.uint8, device=dev),
+                               _empty(stream, (nb, rows), dtype=torch.float32, device=dev))
+        row = (_shaped(codes, "codes", (torch.uint8,), (rows, cols), dev),
+               _shaped(scale, "scale", (torch.float32,), (nb, rows), dev))
+    else:
+        row = None
+    if offsets is not None:
+        G = _offsets(offsets, dev)
+        Pc = bsq_colwise_padded_cols(G, rows)
+        tc, ts = t or (_empty(stream, (cols, Pc), dtype=torch.uint8, device=dev),
+                       _empty(stream, (Pc // 128, cols), dtype=torch.float32, device=dev))
+        t = (_shaped(tc, "t codes", (torch.uint8,), (cols, Pc), dev),
+             _shaped(ts, "t scale", (torch.float32,), (Pc // 128, cols), dev))
+    else:
+        t = None
+    rq, tq = row or (None, None), t or (None, None)
+    _check("bsq_quantize_fp8b128",
+           _lib.bsq_quantize_fp8b128(_ptr(x), src_rows, cols, max(ld, cols), _ptr(row_index), rows, _ptr(offsets), G,
+                                     _ptr(rq[0]), _ptr(rq[1]), _ptr(tq[0]), _ptr(tq[1]), _stream(stream)))
+    return row, t
+
+
+def bsq_quantize_fp8b128_weights(w, num_experts, transposed=True, codes=None, codes_t=None, scale=None, stream=None):
+    """FP8B128 of expert weights ``w`` bf16 [num_experts * n, k] in 128 x 128 blocks:
+    (codes u8 [E*n, k], codes_t u8 [E*k, n] or None, scale f32 [E, ceil(n/128), ceil(k/128)])."""
+    _dev(w, "w", _BF16)
+    rows, k, ld = _rows_ld(w)
+    if num_experts < 1 or rows % num_experts:
+        raise ValueError("w must hold num_experts * n rows")
+    n, dev = rows // num_experts, w.device
+    sshape = (num_experts, (n + 127) // 128, (k + 127) // 128)
+    codes = _empty(stream, (rows, k), dtype=torch.uint8, device=dev) if codes is None else codes
+    scale = _empty(stream, sshape, dtype=torch.float32, device=dev) if scale is None else scale
+    if transposed and codes_t is None:
+        codes_t = _empty(stream, (num_experts * k, n), dtype=torch.uint8, device=dev)
+    _shaped(codes, "codes", (torch.uint8,), (rows, k), dev)
+    _shaped(scale, "scale", (torch.float32,), sshape, dev)
+    if codes_t is not None:
+        _shaped(codes_t, "codes_t", (torch.uint8,), (num_experts * k, n), dev)
+    _check("bsq_quantize_fp8b128_weights",
+           _lib.bsq_quantize_fp8b128_weights(_ptr(w), num_experts, n, k, max(ld, k), _ptr(codes), _ptr(codes_t),
+                                             _ptr(scale), _stream(stream)))
+    return codes, codes_t, scale
 
 
 def bsq_debug_status(workspace, stream=None):

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsq.so")
 
-SOURCES = ["quantize.hip", "plan.hip", "gemm_fwd.hip", "gemm_bwd.hip", "abi.cpp", "noalloc.hip"]
+SOURCES = ["quantize.hip", "plan.hip", "gemm_fwd.hip", "gemm_bwd.hip", "abi.cpp", "noalloc.hip",
+           "moe_route.hip", "moe_dispatch.hip", "quantize_b128.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

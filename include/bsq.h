@@ -72,7 +72,9 @@ typedef struct ihipStream_t* hipStream_t;
  * added bsq_quantize_mxfp8_dual and bsq_grouped_gemm_w4a16.
  * 4: added bsq_grouped_gemm_fwd_noalloc.
  * 5: added bsq_grouped_gemm_fwd_swiglu; the SwiGLU activation's reciprocal
- *    (1 + e^-|g|)^-1 comes from the hardware reciprocal. */
+ *    (1 + e^-|g|)^-1 comes from the hardware reciprocal.
+ * Entry points added since leave those before them as they were, and the
+ * version with them. */
 #define BSQ_ABI_VERSION 5
 
 typedef enum {
@@ -394,6 +396,125 @@ bsq_status bsq_grouped_gemm_w4a16(const void* x_bf16, const uint8_t* w_codes, co
                                   const float* w_rscale, const int32_t* offsets, int32_t num_experts,
                                   int64_t m_total, int64_t n, int64_t k, void* y, bsq_dtype y_dtype,
                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * bsq_moe_route -- top-k routing of router logits, with the balance loss and
+ * the per-expert counts: what fills the expert-sorted shard the grouped GEMMs
+ * work on.  Per token t, with logits l (binary32) and selection bias b:
+ *   key_e = l_e + b_e; the top_k largest keys choose the experts, in
+ *   descending order, ties to the lowest index.  NaN counts as -inf and +inf
+ *   as the largest finite value; an expert whose key is -inf is never chosen.
+ *   A token with fewer than top_k such experts gets id -1 and weight 0 in the
+ *   places left, and one with none (or whose mask byte is 0, then its logits
+ *   are not read) routes nowhere: lse -inf.
+ *   p = softmax(l), lse = log sum_e exp(l_e).  weights = scale * p of the
+ *   chosen experts, or with `normalize` scale * (softmax over the chosen).
+ * With f_e the tokens that chose e, V the tokens that chose any and P_e =
+ * (1/V) sum_t p_te over those:  loss = loss_coef * E / (top_k V) sum_e f_e P_e.
+ *   logits [tokens][ld] in dtype; bias [E] f32 or NULL; mask [tokens] u8 or
+ *   NULL.  expert_ids, weights [tokens][top_k], lse [tokens], counts [E + 1]
+ *   (f, then V), loss [1]: outputs.
+ *   num_experts <= 1024, top_k <= min(64, num_experts).
+ *   workspace >= bsq_moe_route_workspace_size(tokens, num_experts) bytes,
+ *   256-byte aligned; scratch.
+ * Sums over tokens run in a fixed order (repeated runs give the same bits).
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes, alignment), WORKSPACE_TOO_SMALL, HIP.
+ */
+bsq_status bsq_moe_route(const void* logits, bsq_dtype dtype, int64_t tokens, int32_t num_experts, int64_t ld,
+                         int32_t top_k, const float* bias, const uint8_t* mask, int32_t normalize, float scale,
+                         float loss_coef, int32_t* expert_ids, float* weights, float* lse, int32_t* counts,
+                         float* loss, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t bsq_moe_route_workspace_size(int64_t tokens, int32_t num_experts);
+
+/*
+ * bsq_moe_route_bwd -- gradient of the logits from those of the weights and of
+ * the loss; the choice of experts and the counts are constants.  logits,
+ * normalize, scale, loss_coef and the outputs expert_ids, weights, lse, counts
+ * are bsq_moe_route's.  With u_e = dloss * loss_coef * E f_e / (top_k V^2):
+ *   normalize: dl_e = p_e (u_e - sum_i p_i u_i) + [e chosen] w_e (dw_e - sum_j w_j dw_j / scale)
+ *   else:      dl_e = p_e (u'_e - sum_i p_i u'_i), u'_e = u_e + [e chosen] scale dw_e
+ *   dweights [tokens][top_k] f32 or NULL (none); dloss [1] f32 (device) or
+ *   NULL (none).  dlogits [tokens][ld_d] in dtype: zero for tokens that route
+ *   nowhere.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+bsq_status bsq_moe_route_bwd(const void* logits, bsq_dtype dtype, int64_t tokens, int32_t num_experts, int64_t ld,
+                             int32_t top_k, const int32_t* expert_ids, const float* weights, const float* lse,
+                             const int32_t* counts, const float* dweights, const float* dloss, int32_t normalize,
+                             float scale, float loss_coef, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/*
+ * bsq_moe_dispatch -- expert-sorted order of the tokens' choices (a stable
+ * counting sort by expert, in token-major order of the choices):
+ *   offsets [E + 1]: as every grouped entry point takes them; offsets[E] is the
+ *     number of choices with an expert.
+ *   row_index [tokens * top_k]: source token of each slot (what the gathering
+ *     quantizers take); -1 in the slots past offsets[E].
+ *   slot [tokens][top_k]: slot of each choice, -1 for a choice without expert.
+ *   expert_ids [tokens][top_k]: an id outside [0, E) is a choice without expert.
+ * num_experts <= 1024, tokens * top_k < 2^31.  workspace >=
+ * bsq_moe_dispatch_workspace_size(...) bytes, 256-byte aligned; scratch.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP.
+ */
+bsq_status bsq_moe_dispatch(const int32_t* expert_ids, int64_t tokens, int32_t top_k, int32_t num_experts,
+                            int32_t* offsets, int32_t* row_index, int32_t* slot, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+size_t bsq_moe_dispatch_workspace_size(int64_t tokens, int32_t top_k, int32_t num_experts);
+
+/*
+ * bsq_moe_combine -- weighted sum of each token's expert outputs:
+ *   y[t] = sum_j weights[t][j] * ye[slot[t][j]], j ascending, in binary32,
+ * rounded once.  A choice whose slot is outside [0, m_total) adds nothing (its
+ * row is not used); weights == NULL means ones (also the gradient of the gather
+ * of the tokens into slots).
+ *   ye [m_total][ld_ye] and y [tokens][ld_y] in dtype, 16-byte aligned,
+ *   width % 8 == 0, pitches % 8 == 0; weights [tokens][top_k] f32.
+ *
+ * bsq_moe_combine_bwd -- dye[slot[t][j]] = weights[t][j] * dy[t] (rounded
+ * once) and dweights[t][j] = sum_c dy[t][c] * ye[slot[t][j]][c] (0 for a
+ * choice without a slot).  With offsets (the dispatch's, device) the rows of
+ * dye from offsets[num_experts] on, which no choice owns, become zero; without
+ * (NULL) they are not written.  dweights == NULL: not computed (ye may be NULL).
+ * No slot may appear twice.
+ * Errors: INVALID_ARG, UNSUPPORTED (width or pitch multiple, alignment), HIP.
+ */
+bsq_status bsq_moe_combine(const void* ye, bsq_dtype dtype, int64_t m_total, int64_t width, int64_t ld_ye,
+                           const int32_t* slot, const float* weights, int64_t tokens, int32_t top_k, void* y,
+                           int64_t ld_y, hipStream_t stream);
+bsq_status bsq_moe_combine_bwd(const void* dy, bsq_dtype dtype, int64_t tokens, int64_t width, int64_t ld_dy,
+                               const void* ye, int64_t m_total, int64_t ld_ye, const int32_t* slot,
+                               const float* weights, int32_t top_k, const int32_t* offsets, int32_t num_experts,
+                               void* dye, int64_t ld_dye, float* dweights, hipStream_t stream);
+
+/*
+ * FP8B128: E4M3 codes with one fp32 scale per 128 elements.  A block with
+ * maximum magnitude a: c = max(a, 2^-100), code = E4M3_RNE_sat(RN32(x *
+ * RN32(448 / c))), scale = RN32(c / 448), or 0 when a == 0.
+ *   rows (activations): 1 x 128 along the row; codes [rows][cols], scale
+ *     block-major [ceil(cols/128)][rows].
+ *   token columns (weight-gradient operands): 128 x 1 down the rows of each
+ *     group, transposed, in the column layout of BSQ_COLWISE_T: t_codes
+ *     [cols][P], t_scale [P/128][cols], P = bsq_colwise_padded_cols(num_groups,
+ *     rows); every byte that holds no element, and its scale, is 0.
+ *   weights: 128 x 128 per expert; codes [E*n][k], codes_t [E*k][n], scale
+ *     [E][ceil(n/128)][ceil(k/128)] (one array for both orientations).
+ *
+ * bsq_quantize_fp8b128 -- row and / or token-column form of x[row_index] (x
+ * itself when row_index is NULL, then rows == src_rows); an index outside
+ * [0, src_rows) gives a zero row.  codes/scale or t_codes/t_scale may be NULL
+ * (not wanted).  offsets/num_groups (device, as for BSQ_COLWISE_T) are needed
+ * for the token columns; rows past offsets[num_groups] are in no column.  With
+ * both forms one read serves both, and offsets[0] must be 0.
+ *   x_bf16 [src_rows][ld_x] 16-byte aligned, ld_x % 8 == 0; cols % 16 == 0.
+ * bsq_quantize_fp8b128_weights -- w_bf16 [E*n][ld_w]; n % 16 == 0, k % 16 == 0;
+ * codes_t may be NULL.
+ * Errors: INVALID_ARG, UNSUPPORTED, HIP.
+ */
+bsq_status bsq_quantize_fp8b128(const void* x_bf16, int64_t src_rows, int64_t cols, int64_t ld_x,
+                                const int32_t* row_index, int64_t rows, const int32_t* offsets, int32_t num_groups,
+                                uint8_t* codes, float* scale, uint8_t* t_codes, float* t_scale, hipStream_t stream);
+bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts, int64_t n, int64_t k, int64_t ld_w,
+                                        uint8_t* codes, uint8_t* codes_t, float* scale, hipStream_t stream);
 
 /* Bytes of workspace the GEMM entry points need (host function, no GPU use).
  * op is BSQ_OP_GEMM_FWD or BSQ_OP_GEMM_BWD; returns 0 for invalid arguments. */
