@@ -58,6 +58,10 @@ _SIGS = {
     "bsq_moe_combine_bwd": ([P, INT, I64, I64, I64, P, I64, I64, P, P, I32, P, I32, P, I64, P, P], INT),
     "bsq_quantize_fp8b128": ([P, I64, I64, I64, P, I64, P, I32, P, P, P, P, P], INT),
     "bsq_quantize_fp8b128_weights": ([P, I32, I64, I64, I64, P, P, P, P], INT),
+    "bsq_grouped_gemm_fp8b128_fwd": ([P, P, P, P, P, I32, I64, I64, I64, P, INT, P, ctypes.c_size_t, P], INT),
+    "bsq_grouped_gemm_fp8b128_bwd": ([P, P, P, P, P, P, P, P, P, I32, I64, I64, I64, P, INT, P, INT, ctypes.c_uint, P,
+                                      ctypes.c_size_t, P], INT),
+    "bsq_grouped_gemm_fp8b128_workspace_size": ([I32], ctypes.c_size_t),
     "bsq_workspace_size": ([INT, I32, I64, I64, I64], ctypes.c_size_t),
     "bsq_colwise_padded_cols": ([I32, I64], I64),
     "bsq_status_string": ([INT], ctypes.c_char_p),
@@ -681,6 +685,86 @@ def bsq_quantize_fp8b128_weights(w, num_experts, transposed=True, codes=None, co
            _lib.bsq_quantize_fp8b128_weights(_ptr(w), num_experts, n, k, max(ld, k), _ptr(codes), _ptr(codes_t),
                                              _ptr(scale), _stream(stream)))
     return codes, codes_t, scale
+
+
+def bsq_grouped_gemm_fp8b128_workspace_size(num_experts):
+    return int(_lib.bsq_grouped_gemm_fp8b128_workspace_size(num_experts))
+
+
+_OUT_DTYPE = {BSQ_BF16: torch.bfloat16, BSQ_F32: torch.float32}
+
+
+def _out(t, name, dtype, shape, dev, stream):
+    if t is None:
+        return _empty(stream, shape, dtype=_OUT_DTYPE[dtype], device=dev)
+    return _shaped(t, name, (_OUT_DTYPE[dtype],), shape, dev)
+
+
+def bsq_grouped_gemm_fp8b128_fwd(a_q, w_q, offsets, y_dtype=BSQ_BF16, y=None, workspace=None, stream=None):
+    """Forward grouped GEMM on FP8B128 operands: a_q = (codes [m_total, k], scale)
+    of the expert-sorted activations in row form, w_q = (codes [E*n, k], scale [E,
+    ceil(n/128), ceil(k/128)]) of the weights.  Returns y [m_total, n]."""
+    a_codes, a_scale = a_q
+    w_codes, w_scale = w_q
+    _dev(a_codes, "a codes", (torch.uint8,))
+    dev = a_codes.device
+    E = _offsets(offsets, dev)
+    M, k = a_codes.shape
+    n = w_codes.shape[0] // E
+    kb = (k + 127) // 128
+    _shaped(a_codes, "a codes", (torch.uint8,), (M, k), dev)
+    _shaped(a_scale, "a scale", (torch.float32,), (kb, M), dev)
+    _shaped(w_codes, "w codes", (torch.uint8,), (E * n, k), dev)
+    _shaped(w_scale, "w scale", (torch.float32,), (E, (n + 127) // 128, kb), dev)
+    y = _out(y, "y", y_dtype, (M, n), dev, stream)
+    workspace = _scratch(bsq_grouped_gemm_fp8b128_workspace_size(E), workspace, dev, stream)
+    _check("bsq_grouped_gemm_fp8b128_fwd",
+           _lib.bsq_grouped_gemm_fp8b128_fwd(_ptr(a_codes), _ptr(a_scale), _ptr(w_codes), _ptr(w_scale),
+                                             _ptr(offsets), E, M, n, k, _ptr(y), y_dtype, _ptr(workspace),
+                                             workspace.numel() * workspace.element_size(), _stream(stream)))
+    return y
+
+
+def bsq_grouped_gemm_fp8b128_bwd(offsets, m_total, n, k, dy_q=None, wt_q=None, dyt_q=None, xt_q=None,
+                                 flags=BSQ_DGRAD | BSQ_WGRAD, dx_dtype=BSQ_BF16, dw_dtype=BSQ_BF16, dx=None, dw=None,
+                                 workspace=None, stream=None):
+    """Backward grouped GEMMs on FP8B128 operands.  dy_q = row form of dY [m_total, n];
+    wt_q = (codes_t [E*k, n], scale) of the weights; dyt_q / xt_q = token-column
+    forms of dY / X with ``offsets``.  Returns (dx, dw)."""
+    _dev(offsets, "offsets", (torch.int32,))
+    dev = offsets.device
+    E = _offsets(offsets, dev)
+    nb, kb = (n + 127) // 128, (k + 127) // 128
+    u8, f32 = (torch.uint8,), (torch.float32,)
+    none = (None, None)
+    if flags & BSQ_DGRAD:
+        if dy_q is None or wt_q is None:
+            raise ValueError("BSQ_DGRAD needs dy_q and wt_q")
+        _shaped(dy_q[0], "dy codes", u8, (m_total, n), dev)
+        _shaped(dy_q[1], "dy scale", f32, (nb, m_total), dev)
+        _shaped(wt_q[0], "wt codes", u8, (E * k, n), dev)
+        _shaped(wt_q[1], "w scale", f32, (E, nb, kb), dev)
+        dx = _out(dx, "dx", dx_dtype, (m_total, k), dev, stream)
+    else:
+        dy_q = wt_q = none
+    if flags & BSQ_WGRAD:
+        if dyt_q is None or xt_q is None:
+            raise ValueError("BSQ_WGRAD needs dyt_q and xt_q")
+        Pc = bsq_colwise_padded_cols(E, m_total)
+        for q, nm, w in ((dyt_q, "dyt", n), (xt_q, "xt", k)):
+            _shaped(q[0], nm + " codes", u8, (w, Pc), dev)
+            _shaped(q[1], nm + " scale", f32, (Pc // 128, w), dev)
+        dw = _out(dw, "dw", dw_dtype, (E, n, k), dev, stream)
+    else:
+        dyt_q = xt_q = none
+    workspace = _scratch(bsq_grouped_gemm_fp8b128_workspace_size(E), workspace, dev, stream)
+    _check("bsq_grouped_gemm_fp8b128_bwd",
+           _lib.bsq_grouped_gemm_fp8b128_bwd(_ptr(dy_q[0]), _ptr(dy_q[1]), _ptr(wt_q[0]), _ptr(wt_q[1]),
+                                             _ptr(dyt_q[0]), _ptr(dyt_q[1]), _ptr(xt_q[0]), _ptr(xt_q[1]),
+                                             _ptr(offsets), E, m_total, n, k, _ptr(dx), dx_dtype, _ptr(dw), dw_dtype,
+                                             flags, _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                             _stream(stream)))
+    return dx, dw
 
 
 def bsq_debug_status(workspace, stream=None):

@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbsq.so")
 
 SOURCES = ["quantize.hip", "plan.hip", "gemm_fwd.hip", "gemm_bwd.hip", "abi.cpp", "noalloc.hip",
-           "moe_route.hip", "moe_dispatch.hip", "quantize_b128.hip"]
+           "moe_route.hip", "moe_dispatch.hip", "quantize_b128.hip", "gemm_b128.hip"]
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 

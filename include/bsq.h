@@ -516,6 +516,41 @@ bsq_status bsq_quantize_fp8b128(const void* x_bf16, int64_t src_rows, int64_t co
 bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts, int64_t n, int64_t k, int64_t ld_w,
                                         uint8_t* codes, uint8_t* codes_t, float* scale, hipStream_t stream);
 
+/*
+ * bsq_grouped_gemm_fp8b128_fwd -- expert grouped GEMM on FP8B128 operands:
+ *   y[m][j] = sum_b a_scale[b][m] w_scale[e][j/128][b] sum_{k in block b} a[m][k] w_e[j][k]
+ * for every row m of expert e's segment (num_experts == 1: a plain product).
+ * A block's 128 products are summed by the matrix core, the blocks in binary32
+ * in ascending order.  Rows past offsets[num_experts] become zero.
+ *   a_codes [m_total][k], w_codes [E*n][k] 16-byte aligned; n % 16 == 0,
+ *   k % 16 == 0; y [m_total][n] in y_dtype.
+ *
+ * bsq_grouped_gemm_fp8b128_bwd -- with dy the gradient of y:
+ *   BSQ_DGRAD: dx[m][j] = sum_b dy_scale[b][m] w_scale[e][b][j/128] sum_{i in b} dy[m][i] w_e[i][j]
+ *     from the row form of dy [m_total][n] and the transposed codes wt_codes
+ *     [E*k][n]; rows past offsets[E] become zero.
+ *   BSQ_WGRAD: dw[e][i][j] = sum_b dyt_scale[b][i] xt_scale[b][j] sum_{m in b} dy[m][i] x[m][j]
+ *     over the 128-token blocks of expert e, from the token-column forms of dy
+ *     ([n][P]) and x ([k][P]); an expert without tokens gets zeros.
+ *   dx [m_total][k], dw [E][n][k].
+ * offsets: 0 = offsets[0] <= ... <= offsets[E] <= m_total; offsets breaking
+ * this make the call do no work (bsq_debug_status on the workspace reports 1).
+ * workspace >= bsq_grouped_gemm_fp8b128_workspace_size(num_experts) bytes,
+ * 256-byte aligned; scratch.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP.
+ */
+bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
+                                        const float* w_scale, const int32_t* offsets, int32_t num_experts,
+                                        int64_t m_total, int64_t n, int64_t k, void* y, bsq_dtype y_dtype,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+bsq_status bsq_grouped_gemm_fp8b128_bwd(const uint8_t* dy_codes, const float* dy_scale, const uint8_t* wt_codes,
+                                        const float* w_scale, const uint8_t* dyt_codes, const float* dyt_scale,
+                                        const uint8_t* xt_codes, const float* xt_scale, const int32_t* offsets,
+                                        int32_t num_experts, int64_t m_total, int64_t n, int64_t k, void* dx,
+                                        bsq_dtype dx_dtype, void* dw, bsq_dtype dw_dtype, unsigned flags,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t bsq_grouped_gemm_fp8b128_workspace_size(int32_t num_experts);
+
 /* Bytes of workspace the GEMM entry points need (host function, no GPU use).
  * op is BSQ_OP_GEMM_FWD or BSQ_OP_GEMM_BWD; returns 0 for invalid arguments. */
 size_t bsq_workspace_size(int op, int32_t num_experts, int64_t m_total, int64_t n, int64_t k);

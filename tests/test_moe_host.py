@@ -94,6 +94,32 @@ def test_quantize(bsq):
     assert w(FAKE, 0, 64, 64, 64, FAKE, FAKE, FAKE, None) == bsq.BSQ_OK
 
 
+def test_gemm(bsq):
+    need = bsq.bsq_grouped_gemm_fp8b128_workspace_size(4)
+    assert need > 0 and bsq.bsq_grouped_gemm_fp8b128_workspace_size(0) == 0
+    assert bsq.bsq_grouped_gemm_fp8b128_workspace_size(4097) == 0
+    inv, uns = bsq.BSQ_ERR_INVALID_ARG, bsq.BSQ_ERR_UNSUPPORTED
+
+    def fwd(a=FAKE, w=FAKE, off=FAKE, E=4, M=64, n=64, k=128, y=FAKE, dt=0, ws=FAKE, wb=need):
+        return bsq._lib.bsq_grouped_gemm_fp8b128_fwd(a, FAKE, w, FAKE, off, E, M, n, k, y, dt, ws, wb, None)
+
+    assert fwd(a=None) == fwd(w=None) == fwd(off=None) == fwd(y=None) == fwd(ws=None) == inv
+    assert fwd(E=0) == fwd(M=-1) == fwd(dt=2) == inv
+    assert fwd(n=0) == fwd(n=72) == fwd(k=120) == fwd(E=4097) == fwd(a=ODD) == fwd(y=ODD) == uns
+    assert fwd(k=1 << 23) == fwd(n=1 << 21) == fwd(M=1 << 29) == uns
+    assert fwd(wb=need - 1) == bsq.BSQ_ERR_WORKSPACE_TOO_SMALL and fwd(M=0) == bsq.BSQ_OK
+
+    def bwd(flags=3, dy=FAKE, wt=FAKE, dyt=FAKE, xt=FAKE, dx=FAKE, dw=FAKE, M=64, n=64, k=128, dt=0, wb=need):
+        return bsq._lib.bsq_grouped_gemm_fp8b128_bwd(dy, FAKE, wt, FAKE, dyt, FAKE, xt, FAKE, FAKE, 4, M, n, k, dx, dt,
+                                                     dw, dt, flags, FAKE, wb, None)
+
+    assert bwd(flags=0) == bwd(flags=4) == bwd(dy=None) == bwd(wt=None) == bwd(dyt=None) == bwd(xt=None) == inv
+    assert bwd(dx=None) == bwd(dw=None) == bwd(dt=3) == inv
+    assert bwd(n=56) == bwd(k=0) == bwd(dw=ODD) == bwd(xt=ODD) == bwd(M=1 << 24) == bwd(k=1 << 21) == uns
+    assert bwd(wb=need - 1) == bsq.BSQ_ERR_WORKSPACE_TOO_SMALL
+    assert bwd(flags=bsq.BSQ_DGRAD, M=0, dw=None) == bsq.BSQ_OK
+
+
 def test_binding_refuses_host_tensors_and_shapes(bsq):
     import torch
     with pytest.raises(TypeError):
