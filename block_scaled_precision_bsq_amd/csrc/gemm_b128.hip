@@ -262,6 +262,289 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         }
 }
 
+// 256 x 256 output tiles: 8 waves, two per SIMD, of 128 x 64 (NI = 8 groups of
+// 16 rows; 4 where the tile has at most 128 rows).  Waves 4..7 issue all DMA,
+// so the matrix work of waves 0..3 never queues behind a DMA instruction that
+// finds the memory queue full.  Two stages are in flight: a wave reads its
+// fragments three row groups ahead, so from group WIDE_X on a slot's data is in
+// registers (barrier X) and the DMA waves refill it with the stage after next,
+// while the next one has until group WIDE_Y (barrier Y) to land.  A sum waits
+// two MFMAs for its product, so the vector units work beside the matrix cores:
+// 16 of an MFMA's 32 cycles forward, 32 for wgrad.  B rows go to LDS in an order
+// that leaves a lane 16 adjacent output columns.
+// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 932 us, 2.06
+// PFLOP/s (128 x 128 tiles: 1472 us); dgrad + wgrad 2351 us (3312 us).
+constexpr int WT = 256;
+struct WideSlot {
+    uint8_t a[WT * 128];
+    uint8_t b[WT * 128];  // row 16 j + 4 q + v of each 64 holds output column 16 q + 4 j + v
+    float sa[WT];
+    float sb[WT];  // wgrad: by output column; else the two 128-column blocks' scales
+};
+constexpr uint32_t WIDE_SLOT = sizeof(WideSlot);
+constexpr int WIDE_X = 5;   // group of 16 rows before which the slot's reads are over (barrier X)
+constexpr int WIDE_Y = 6;   // and before which the next stage is needed (barrier Y)
+constexpr int WIDE_PARTS = 9;
+constexpr int64_t WIDE_MIN_TILES = 512;
+
+template <bool OUT_F32, bool WGRAD>
+__global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
+    extern __shared__ __align__(16) uint8_t s_wide[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const bool dwave = wave >= 4;
+    const int dw = wave & 3;
+    const int wm = wave & 1, wn = wave >> 1;
+    const int CT = (int)((p.C + WT - 1) / WT);
+    // 32 consecutive tiles (4 row tiles x 8 column tiles) to an XCD at a time
+    const int64_t t = (((int64_t)blockIdx.x >> 8) * 8 + (blockIdx.x & 7)) * 32 + ((blockIdx.x >> 3) & 31);
+    int e, rows;
+    int64_t r0, R;
+    const uint8_t *a, *b;
+    const float *as, *bs;
+    int64_t lda, ldas, ldbs;
+    char* out;
+    int c0;
+    if constexpr (!WGRAD) {
+        const int64_t g = t / (4 * CT);
+        const int l = (int)(t - g * 4 * CT);
+        const RowTile f = find_row_tile<WT>(p, g * 4 + (l & 3), lane);
+        if (f.e < 0) return;
+        e = f.e;
+        r0 = f.row0;
+        rows = (int)min((int64_t)WT, f.end - r0);
+        c0 = WT * (l >> 2);
+        R = e < p.E ? p.R : 0;
+        const int64_t we = e < p.E ? e : 0;
+        a = p.a + r0 * p.R;
+        lda = p.R;
+        as = p.as + r0;
+        ldas = p.M;
+        b = p.b + (we * p.C + c0) * p.R;
+        bs = p.bs + we * p.bs_e + (int64_t)(c0 / 128) * p.bs_c;
+        ldbs = p.bs_b;
+        out = static_cast<char*>(p.out) + (r0 * p.C + c0) * (OUT_F32 ? 4 : 2);
+    } else {
+        const int RT = (int)((p.R + WT - 1) / WT);
+        if (t >= (int64_t)p.E * RT * CT) return;
+        e = (int)(t / (RT * CT));
+        const int l = (int)(t - (int64_t)e * RT * CT);
+        const int g = l / (4 * CT), h = min(4, RT - 4 * g);
+        const int ll = l - g * 4 * CT;
+        r0 = WT * (4 * g + ll % h);
+        c0 = WT * (ll / h);
+        rows = (int)min((int64_t)WT, p.R - r0);
+        // the whole call is dropped where any offset is invalid
+        bool bad = p.offsets[0] != 0 || p.offsets[p.E] > p.M;
+        for (int i = lane; i < p.E; i += 64) bad |= p.offsets[i + 1] < p.offsets[i];
+        bad = __ballot(bad) != 0;
+        if (t == 0 && threadIdx.x == 0) *p.err = bad ? 1 : 0;
+        if (bad) return;
+        const int64_t o0 = p.offsets[e];
+        R = p.offsets[e + 1] - o0;
+        const int64_t blk = e + o0 / 128;
+        a = p.a + r0 * p.P + 128 * blk;
+        lda = p.P;
+        as = p.as + blk * p.R + r0;
+        ldas = p.R;
+        b = p.b + (int64_t)c0 * p.P + 128 * blk;
+        bs = p.bs + blk * p.C + c0;
+        ldbs = p.C;
+        out = static_cast<char*>(p.out) + (((int64_t)e * p.R + r0) * p.C + c0) * (OUT_F32 ? 4 : 2);
+    }
+    rows = __builtin_amdgcn_readfirstlane(rows);
+    const int cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)WT, p.C - c0));
+    const int nb = __builtin_amdgcn_readfirstlane((int)((R + 127) / 128));
+    const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)lda);
+    const uint32_t lsa = __builtin_amdgcn_readfirstlane((uint32_t)ldas), lsb = __builtin_amdgcn_readfirstlane((uint32_t)ldbs);
+    // token columns are padded to whole blocks of zeros; k and n are not
+    const uint32_t len = WGRAD ? (uint32_t)nb * 128u : __builtin_amdgcn_readfirstlane((uint32_t)R);
+    // rows past the tile lie past the descriptors' ranges
+    const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(a), (uint32_t)rows * ld), rb = rsrc_n(uniform_ptr(b), (uint32_t)cols * ld);
+    const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(as), 0x7FFFFFFFu), rsb = rsrc_n(uniform_ptr(bs), 0x7FFFFFFFu);
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(s_wide));
+    const __attribute__((address_space(3))) uint8_t* lds = (const __attribute__((address_space(3))) uint8_t*)(s_wide);
+
+    // DMA of stage s into slot s & 1 by DMA wave dw, in parts of two
+    // instructions: parts 0..7 eight rows of either operand, part 8 the scales.
+    // prep(s) sets the lane offsets of stage s: chunk (lane & 7) ^ swz8(row) of
+    // the rows 8 i + lane / 8, even and odd i, or nowhere past the last stage.
+    const int drow = lane >> 3;
+    const uint32_t ch0 = 16u * (uint32_t)((lane & 7) ^ swz8(drow)), ch1 = 16u * (uint32_t)((lane & 7) ^ swz8(8 + drow));
+    const uint32_t abase = (uint32_t)(64 * dw + drow) * ld;
+    const uint32_t bbase = (uint32_t)(64 * dw + 16 * (drow >> 2) + (drow & 3)) * ld;
+    const uint32_t bsoff = WGRAD ? (64 * dw + lane < cols ? 4u * (uint32_t)(64 * dw + lane) : OOB)
+                                 : ((dw == 0 && lane < (cols + 127) / 128) ? 4u * (uint32_t)(lane * p.bs_c) : OOB);
+    const uint32_t asoff = 64 * dw + lane < rows ? 4u * (uint32_t)(64 * dw + lane) : OOB;
+    uint32_t va[2], vb[2];
+    auto prep = [&](int s) {
+        const uint32_t k0 = 128u * (uint32_t)s + ch0, k1 = 128u * (uint32_t)s + ch1;
+        va[0] = k0 < len ? abase + k0 : OOB;
+        va[1] = k1 < len ? abase + k1 : OOB;
+        vb[0] = k0 < len ? bbase + k0 : OOB;
+        vb[1] = k1 < len ? bbase + k1 : OOB;
+    };
+    auto issue = [&](int s, int part) {
+        const uint32_t slot = lds0 + (uint32_t)(s & 1) * WIDE_SLOT;
+        if (part < 8) {
+            const int i = part;
+            // LDS row 8 i + lane / 8 of the 64: j = i / 2, q = 2 (i & 1) + lane / 32
+            const uint32_t brow = (uint32_t)(4 * (i >> 1) + 32 * (i & 1));
+            dma_lds_r<16>(ra, va[i & 1] + (uint32_t)(8 * i) * ld,
+                          slot + 8192u * (uint32_t)dw + (uint32_t)offsetof(WideSlot, a) + 1024u * (uint32_t)i);
+            dma_lds_r<16>(rb, vb[i & 1] + brow * ld,
+                          slot + 8192u * (uint32_t)dw + (uint32_t)offsetof(WideSlot, b) + 1024u * (uint32_t)i);
+        } else {
+            const uint32_t ao = 4u * (uint32_t)s * lsa, bo = 4u * (uint32_t)s * lsb;
+            const bool ok = s < nb;
+            dma_lds_r<4>(rsa, ok ? asoff + ao : OOB, slot + (uint32_t)offsetof(WideSlot, sa) + 256u * (uint32_t)dw);
+            dma_lds_r<4>(rsb, ok ? bsoff + bo : OOB, slot + (uint32_t)offsetof(WideSlot, sb) + 256u * (uint32_t)dw);
+        }
+    };
+
+    if (dwave) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            prep(s);
+#pragma unroll
+            for (int i = 0; i < WIDE_PARTS; ++i) issue(s, i);
+        }
+    }
+    const int lr = lane & 15, q = lane >> 4;
+    const uint32_t fr = (uint32_t)(128 * lr + 16 * (q ^ swz8(lr)));
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
+    const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
+
+    auto body = [&](auto NIC, auto DWC) {
+        constexpr int NI = decltype(NIC)::value;
+        constexpr bool DW = decltype(DWC)::value != 0;
+        constexpr int XI = WIDE_X - (8 - NI), YI = WIDE_Y - (8 - NI);
+        const uint32_t fa = (uint32_t)offsetof(WideSlot, a) + (uint32_t)(wm * NI * 16 * 128) + fr, fa1 = fa ^ 64u;
+        const uint32_t fb = (uint32_t)offsetof(WideSlot, b) + (uint32_t)(wn * 64 * 128) + fr, fb1 = fb ^ 64u;
+        const uint32_t fsa = (uint32_t)offsetof(WideSlot, sa) + 4u * (uint32_t)(wm * NI * 16 + lr);
+        const uint32_t fsb = (uint32_t)offsetof(WideSlot, sb) + (WGRAD ? 4u * (uint32_t)(64 * wn + 16 * q) : 4u * (uint32_t)(wn >> 1));
+        auto frag = [&](uint32_t at, uint32_t at1) {
+            const u32x4 x0 = *(const __attribute__((address_space(3))) u32x4*)(lds + at);
+            const u32x4 x1 = *(const __attribute__((address_space(3))) u32x4*)(lds + at1);
+            return int8v{(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+        };
+        auto f32_at = [&](uint32_t at) { return *(const __attribute__((address_space(3))) float*)(lds + at); };
+        float4v acc[NI][4], D[4], sB[4];
+        int8v A[4], B[4];
+        float sa[4], sw = 0.0f, sc = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            D[j] = sB[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < NI; ++i) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        auto rdA = [&](int s, int i) {
+            const uint32_t slot = (uint32_t)(s & 1) * WIDE_SLOT;
+            A[i & 3] = frag(slot + fa + 2048u * (uint32_t)i, slot + fa1 + 2048u * (uint32_t)i);
+            sa[i & 3] = f32_at(slot + fsa + 64u * (uint32_t)i);
+        };
+        auto rdB = [&](int s, int j) {
+            const uint32_t slot = (uint32_t)(s & 1) * WIDE_SLOT + 2048u * (uint32_t)j;
+            B[j] = frag(slot + fb, slot + fb1);
+        };
+        auto rdS = [&](int s, int j) {
+            if constexpr (WGRAD)
+                sB[j] = *(const __attribute__((address_space(3))) float4v*)(lds + (uint32_t)(s & 1) * WIDE_SLOT + fsb + 16u * (uint32_t)j);
+        };
+        auto add = [&](int i, int j, float c) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(WGRAD ? D[j][v] * sB[j][v] : D[j][v], c, acc[i][j][v]);
+        };
+        // stages 0 and 1 are in flight
+        if (DW) wait_vmcnt<2 * WIDE_PARTS>();
+        block_barrier();
+#pragma unroll
+        for (int i = 0; i < 3; ++i) rdA(0, i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) rdB(0, j);
+        if constexpr (!WGRAD) sw = f32_at(fsb);
+        rdS(0, 0);
+        rdS(0, 1);
+        for (int s = 0; s < nb; ++s) {
+            // Slot m = 4 i + j: MFMA (i, j), then the sum of the MFMA two
+            // slots back, so that no sum waits for the matrix core.
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                if (i == XI) {
+                    wait_lgkmcnt0();
+                    block_barrier();
+                }
+                if (i == YI) {
+                    if (DW) wait_vmcnt<8 * (YI - XI)>();  // two instructions behind each MFMA since X
+                    block_barrier();
+                }
+                const float sc_i = WGRAD ? sa[i & 3] : sa[i & 3] * sw;
+                if constexpr (!WGRAD)
+                    if (i == NI - 1) sw = f32_at((uint32_t)((s + 1) & 1) * WIDE_SLOT + fsb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = 4 * i + j;
+                    const float4v d = b128_mfma(B[j], A[i & 3]);
+                    // the sum two slots back
+                    if (j >= 2) add(i, j - 2, sc_i);
+                    else add((i + NI - 1) % NI, j + 2, sc);
+                    D[j] = d;
+                    if (i == 0 && j < 2) rdS(s, j + 2);
+                    if (i == NI - 1 && j >= 2) rdS(s + 1, j - 2);
+                    if (j == 0 && i + 3 < NI) rdA(s, i + 3);
+                    if (i >= YI && i + 3 >= NI) {
+                        // next stage's first three row groups once their registers are free
+                        if (i == YI && YI == NI - 2) {
+                            if (j == 1) rdA(s + 1, 0);
+                            if (j == 3) rdA(s + 1, 1);
+                        }
+                        if (i == NI - 1) {
+                            if (j == 0) rdA(s + 1, 2);
+                            rdB(s + 1, j);
+                        }
+                    }
+                    if (DW) {
+                        const int at = m - 4 * XI;
+                        if (at == 0) prep(s + 2);
+                        if (at >= 0 && at < WIDE_PARTS) issue(s + 2, at);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                sc = sc_i;
+            }
+        }
+        add(NI - 1, 2, sc);
+        add(NI - 1, 3, sc);
+        if (DW) wait_vmcnt<0>();
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            const int r = wm * NI * 16 + 16 * i + lr, c = 64 * wn + 16 * q;
+            const uint32_t o = (r < rows && c < cols) ? (uint32_t)r * ldo + (uint32_t)c * (OUT_F32 ? 4u : 2u) : OOB;
+            if constexpr (OUT_F32) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), ro, (int)(o + 16u * j), 0, 0);
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        u32x4{pack_bf16x2(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16x2(acc[i][2 * h][2], acc[i][2 * h][3]),
+                              pack_bf16x2(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                              pack_bf16x2(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])},
+                        ro, (int)(o + 16u * h), 0, 0);
+            }
+        }
+    };
+    if (rows > 128) {
+        if (dwave) body(IC<8>{}, IC<1>{});
+        else body(IC<8>{}, IC<0>{});
+    } else {
+        if (dwave) body(IC<4>{}, IC<1>{});
+        else body(IC<4>{}, IC<0>{});
+    }
+}
+
 namespace {
 
 constexpr int64_t kMaxOffset = (int64_t)1 << 31;  // 32-bit buffer offsets
@@ -271,8 +554,30 @@ bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (
 // Most row tiles of TM rows that E experts and the rows past them can need.
 int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M : E + 1); }
 
+template <bool F32, bool WGRAD>
+bsq_status launch_wide(const B128Args& a, int64_t tiles, hipStream_t s) {
+    const int64_t grid = (tiles + 255) / 256 * 256;
+    if (grid * 512 >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
+    static bool attr_set = false;  // idempotent; racing writers set the same value
+    if (!attr_set) {
+        if (hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_b128_wide<F32, WGRAD>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, 2 * WIDE_SLOT) != hipSuccess)
+            return BSQ_ERR_HIP;
+        attr_set = true;
+    }
+    hipLaunchKernelGGL((k_gemm_b128_wide<F32, WGRAD>), dim3((unsigned)grid), dim3(512), 2 * WIDE_SLOT, s, a);
+    return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
+}
+
 template <bool WGRAD>
 bsq_status launch_b128(const B128Args& a, bool f32, hipStream_t s) {
+    {
+        const int64_t wct = (a.C + WT - 1) / WT;
+        const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + WT - 1) / WT) * wct
+                                    : (max_row_tiles(a.M, a.E, WT) + 3) / 4 * 4 * wct;
+        if (tiles >= WIDE_MIN_TILES)
+            return f32 ? launch_wide<true, WGRAD>(a, tiles, s) : launch_wide<false, WGRAD>(a, tiles, s);
+    }
     const int64_t ct = (a.C + BT - 1) / BT;
     int64_t grid;
     if (WGRAD)
