@@ -263,17 +263,22 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 }
 
 // 256 x 256 output tiles: 8 waves, two per SIMD, of 128 x 64 (NI = 8 groups of
-// 16 rows; 4 where the tile has at most 128 rows).  Waves 4..7 issue all DMA,
-// so the matrix work of waves 0..3 never queues behind a DMA instruction that
-// finds the memory queue full.  Two stages are in flight: a wave reads its
-// fragments three row groups ahead, so from group WIDE_X on a slot's data is in
-// registers (barrier X) and the DMA waves refill it with the stage after next,
-// while the next one has until group WIDE_Y (barrier Y) to land.  A sum waits
-// two MFMAs for its product, so the vector units work beside the matrix cores:
-// 16 of an MFMA's 32 cycles forward, 32 for wgrad.  B rows go to LDS in an order
-// that leaves a lane 16 adjacent output columns.
-// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 932 us, 2.06
-// PFLOP/s (128 x 128 tiles: 1472 us); dgrad + wgrad 2351 us (3312 us).
+// 16 rows; 4 where the tile has at most 128 rows).
+// The stream of operands bounds the loop (its DMA alone takes 69% of the time,
+// its matrix work alone 67%): a compute unit's first-level cache keeps a fixed
+// number of lines in flight and an instruction that finds it full stalls its
+// wave.  So two stages are in flight, and every wave issues its share of a
+// stage's DMA spread over 18 MFMAs (over 9: 992 us in the case below, over 24:
+// 909; all of it in four waves of the eight, over 9 / 24: 928 / 896, at twice
+// the code and, for wgrad, more registers than there are).  A wave reads its
+// fragments three row groups ahead: WIDE_X MFMAs before a stage's end its data
+// is in registers (barrier X) and its slot is refilled with the stage after
+// next, while the next one has until WIDE_Y MFMAs before the end (barrier Y) to
+// land.  A sum waits two MFMAs for its product, so the vector units work beside
+// the matrix cores: 16 of an MFMA's 32 cycles forward, 32 for wgrad.  B rows go
+// to LDS in an order that leaves a lane 16 adjacent output columns.
+// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 903 us, 2.13
+// PFLOP/s (128 x 128 tiles: 1472 us); dgrad 931 us, wgrad 1400 us.
 constexpr int WT = 256;
 struct WideSlot {
     uint8_t a[WT * 128];
@@ -282,18 +287,28 @@ struct WideSlot {
     float sb[WT];  // wgrad: by output column; else the two 128-column blocks' scales
 };
 constexpr uint32_t WIDE_SLOT = sizeof(WideSlot);
-constexpr int WIDE_X = 5;   // group of 16 rows before which the slot's reads are over (barrier X)
-constexpr int WIDE_Y = 6;   // and before which the next stage is needed (barrier Y)
-constexpr int WIDE_PARTS = 9;
+constexpr int WIDE_X = 12;  // MFMAs before a stage's end at which the slot's reads are over (barrier X)
+constexpr int WIDE_Y = 8;   // and at which the next stage is needed (barrier Y)
+constexpr int WIDE_DMA = 9;  // DMA instructions per wave and stage
+constexpr int WIDE_SPREAD = 18;  // MFMAs over which they go out (half as many in the half-height loop)
 constexpr int64_t WIDE_MIN_TILES = 512;
+
+// DMA instruction n of a stage goes out behind the wide_due(n)th MFMA after X
+// (counted through to the next stage); wide_sent(m): how many go before the mth.
+template <int NI>
+constexpr int wide_due(int n) { return n * (WIDE_SPREAD * NI / 8) / WIDE_DMA; }
+template <int NI>
+constexpr int wide_sent(int m) {
+    int c = 0;
+    for (int n = 0; n < WIDE_DMA; ++n) c += wide_due<NI>(n) < m;
+    return c;
+}
 
 template <bool OUT_F32, bool WGRAD>
 __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     extern __shared__ __align__(16) uint8_t s_wide[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const bool dwave = wave >= 4;
-    const int dw = wave & 3;
     const int wm = wave & 1, wn = wave >> 1;
     const int CT = (int)((p.C + WT - 1) / WT);
     // 32 consecutive tiles (4 row tiles x 8 column tiles) to an XCD at a time
@@ -365,17 +380,23 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(s_wide));
     const __attribute__((address_space(3))) uint8_t* lds = (const __attribute__((address_space(3))) uint8_t*)(s_wide);
 
-    // DMA of stage s into slot s & 1 by DMA wave dw, in parts of two
-    // instructions: parts 0..7 eight rows of either operand, part 8 the scales.
+    // DMA of stage s into slot s & 1: instructions 2 i and 2 i + 1 move eight
+    // rows of either operand, 8 the scales.
     // prep(s) sets the lane offsets of stage s: chunk (lane & 7) ^ swz8(row) of
     // the rows 8 i + lane / 8, even and odd i, or nowhere past the last stage.
     const int drow = lane >> 3;
     const uint32_t ch0 = 16u * (uint32_t)((lane & 7) ^ swz8(drow)), ch1 = 16u * (uint32_t)((lane & 7) ^ swz8(8 + drow));
-    const uint32_t abase = (uint32_t)(64 * dw + drow) * ld;
-    const uint32_t bbase = (uint32_t)(64 * dw + 16 * (drow >> 2) + (drow & 3)) * ld;
-    const uint32_t bsoff = WGRAD ? (64 * dw + lane < cols ? 4u * (uint32_t)(64 * dw + lane) : OOB)
-                                 : ((dw == 0 && lane < (cols + 127) / 128) ? 4u * (uint32_t)(lane * p.bs_c) : OOB);
-    const uint32_t asoff = 64 * dw + lane < rows ? 4u * (uint32_t)(64 * dw + lane) : OOB;
+    const uint32_t abase = (uint32_t)(32 * wave + drow) * ld;
+    const uint32_t bbase = (uint32_t)(64 * (wave >> 1) + 8 * (wave & 1) + 16 * (drow >> 2) + (drow & 3)) * ld;
+    // scales: waves 0..3 those of A, waves 4..7 those of B
+    const int srow = 64 * (wave & 3) + lane;
+    const bool sb_wave = wave >= 4;
+    const __amdgpu_buffer_rsrc_t rsc = sb_wave ? rsb : rsa;
+    const uint32_t lsc = sb_wave ? lsb : lsa;
+    const uint32_t scoff = sb_wave ? (WGRAD ? (srow < cols ? 4u * (uint32_t)srow : OOB)
+                                            : (srow < (cols + 127) / 128 ? 4u * (uint32_t)(srow * p.bs_c) : OOB))
+                                   : (srow < rows ? 4u * (uint32_t)srow : OOB);
+    const uint32_t scdst = (uint32_t)(sb_wave ? offsetof(WideSlot, sb) : offsetof(WideSlot, sa)) + 256u * (uint32_t)(wave & 3);
     uint32_t va[2], vb[2];
     auto prep = [&](int s) {
         const uint32_t k0 = 128u * (uint32_t)s + ch0, k1 = 128u * (uint32_t)s + ch1;
@@ -384,42 +405,34 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         vb[0] = k0 < len ? bbase + k0 : OOB;
         vb[1] = k1 < len ? bbase + k1 : OOB;
     };
-    auto issue = [&](int s, int part) {
+    auto issue = [&](int s, int n) {
         const uint32_t slot = lds0 + (uint32_t)(s & 1) * WIDE_SLOT;
-        if (part < 8) {
-            const int i = part;
+        const int i = n >> 1;
+        if (n == 8) {
+            dma_lds_r<4>(rsc, s < nb ? scoff + 4u * (uint32_t)s * lsc : OOB, slot + scdst);
+        } else if (n & 1) {
             // LDS row 8 i + lane / 8 of the 64: j = i / 2, q = 2 (i & 1) + lane / 32
             const uint32_t brow = (uint32_t)(4 * (i >> 1) + 32 * (i & 1));
-            dma_lds_r<16>(ra, va[i & 1] + (uint32_t)(8 * i) * ld,
-                          slot + 8192u * (uint32_t)dw + (uint32_t)offsetof(WideSlot, a) + 1024u * (uint32_t)i);
             dma_lds_r<16>(rb, vb[i & 1] + brow * ld,
-                          slot + 8192u * (uint32_t)dw + (uint32_t)offsetof(WideSlot, b) + 1024u * (uint32_t)i);
+                          slot + 4096u * (uint32_t)wave + (uint32_t)offsetof(WideSlot, b) + 1024u * (uint32_t)i);
         } else {
-            const uint32_t ao = 4u * (uint32_t)s * lsa, bo = 4u * (uint32_t)s * lsb;
-            const bool ok = s < nb;
-            dma_lds_r<4>(rsa, ok ? asoff + ao : OOB, slot + (uint32_t)offsetof(WideSlot, sa) + 256u * (uint32_t)dw);
-            dma_lds_r<4>(rsb, ok ? bsoff + bo : OOB, slot + (uint32_t)offsetof(WideSlot, sb) + 256u * (uint32_t)dw);
+            dma_lds_r<16>(ra, va[i & 1] + (uint32_t)(8 * i) * ld,
+                          slot + 4096u * (uint32_t)wave + (uint32_t)offsetof(WideSlot, a) + 1024u * (uint32_t)i);
         }
     };
 
-    if (dwave) {
-        __builtin_amdgcn_s_setprio(1);
+    prep(0);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            prep(s);
-#pragma unroll
-            for (int i = 0; i < WIDE_PARTS; ++i) issue(s, i);
-        }
-    }
+    for (int n = 0; n < WIDE_DMA; ++n) issue(0, n);
+    prep(1);
     const int lr = lane & 15, q = lane >> 4;
     const uint32_t fr = (uint32_t)(128 * lr + 16 * (q ^ swz8(lr)));
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
     const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
 
-    auto body = [&](auto NIC, auto DWC) {
+    auto body = [&](auto NIC) {
         constexpr int NI = decltype(NIC)::value;
-        constexpr bool DW = decltype(DWC)::value != 0;
-        constexpr int XI = WIDE_X - (8 - NI), YI = WIDE_Y - (8 - NI);
+        constexpr int NM = 4 * NI, XM = NM - WIDE_X, YM = NM - WIDE_Y;
         const uint32_t fa = (uint32_t)offsetof(WideSlot, a) + (uint32_t)(wm * NI * 16 * 128) + fr, fa1 = fa ^ 64u;
         const uint32_t fb = (uint32_t)offsetof(WideSlot, b) + (uint32_t)(wn * 64 * 128) + fr, fb1 = fb ^ 64u;
         const uint32_t fsa = (uint32_t)offsetof(WideSlot, sa) + 4u * (uint32_t)(wm * NI * 16 + lr);
@@ -456,8 +469,10 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(WGRAD ? D[j][v] * sB[j][v] : D[j][v], c, acc[i][j][v]);
         };
-        // stages 0 and 1 are in flight
-        if (DW) wait_vmcnt<2 * WIDE_PARTS>();
+        // stage 0 and the first instructions of stage 1 are in flight
+#pragma unroll
+        for (int n = 0; n < wide_sent<NI>(NM - XM); ++n) issue(1, n);
+        wait_vmcnt<wide_sent<NI>(NM - XM)>();
         block_barrier();
 #pragma unroll
         for (int i = 0; i < 3; ++i) rdA(0, i);
@@ -471,20 +486,20 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
             // slots back, so that no sum waits for the matrix core.
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                if (i == XI) {
-                    wait_lgkmcnt0();
-                    block_barrier();
-                }
-                if (i == YI) {
-                    if (DW) wait_vmcnt<8 * (YI - XI)>();  // two instructions behind each MFMA since X
-                    block_barrier();
-                }
                 const float sc_i = WGRAD ? sa[i & 3] : sa[i & 3] * sw;
                 if constexpr (!WGRAD)
                     if (i == NI - 1) sw = f32_at((uint32_t)((s + 1) & 1) * WIDE_SLOT + fsb);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int m = 4 * i + j;
+                    if (m == XM) {
+                        wait_lgkmcnt0();
+                        block_barrier();
+                    }
+                    if (m == YM) {
+                        wait_vmcnt<wide_sent<NI>(YM - XM)>();
+                        block_barrier();
+                    }
                     const float4v d = b128_mfma(B[j], A[i & 3]);
                     // the sum two slots back
                     if (j >= 2) add(i, j - 2, sc_i);
@@ -493,22 +508,17 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
                     if (i == 0 && j < 2) rdS(s, j + 2);
                     if (i == NI - 1 && j >= 2) rdS(s + 1, j - 2);
                     if (j == 0 && i + 3 < NI) rdA(s, i + 3);
-                    if (i >= YI && i + 3 >= NI) {
-                        // next stage's first three row groups once their registers are free
-                        if (i == YI && YI == NI - 2) {
-                            if (j == 1) rdA(s + 1, 0);
-                            if (j == 3) rdA(s + 1, 1);
-                        }
-                        if (i == NI - 1) {
-                            if (j == 0) rdA(s + 1, 2);
-                            rdB(s + 1, j);
-                        }
+                    // next stage's first fragments once their registers are free
+                    if (m == YM) rdA(s + 1, 0);
+                    if (m == YM + 2) rdA(s + 1, 1);
+                    if (i == NI - 1) {
+                        if (j == 0) rdA(s + 1, 2);
+                        rdB(s + 1, j);
                     }
-                    if (DW) {
-                        const int at = m - 4 * XI;
-                        if (at == 0) prep(s + 2);
-                        if (at >= 0 && at < WIDE_PARTS) issue(s + 2, at);
-                    }
+                    if (m == XM) prep(s + 2);
+#pragma unroll
+                    for (int n = 0; n < WIDE_DMA; ++n)
+                        if (wide_due<NI>(n) == (m >= XM ? m - XM : m - XM + NM)) issue(s + (m >= XM ? 2 : 1), n);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 sc = sc_i;
@@ -516,7 +526,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         }
         add(NI - 1, 2, sc);
         add(NI - 1, 3, sc);
-        if (DW) wait_vmcnt<0>();
+        wait_vmcnt<0>();
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             const int r = wm * NI * 16 + 16 * i + lr, c = 64 * wn + 16 * q;
@@ -536,13 +546,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
             }
         }
     };
-    if (rows > 128) {
-        if (dwave) body(IC<8>{}, IC<1>{});
-        else body(IC<8>{}, IC<0>{});
-    } else {
-        if (dwave) body(IC<4>{}, IC<1>{});
-        else body(IC<4>{}, IC<0>{});
-    }
+    if (rows > 128) body(IC<8>{});
+    else body(IC<4>{});
 }
 
 namespace {
