@@ -10,6 +10,7 @@ importing this package fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -90,8 +91,8 @@ def _check(fn, status):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    # the raw handle: building a torch.cuda.Stream costs 3 us, a third of a small call
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
 def _empty(stream, shape, dtype, device):
@@ -104,8 +105,25 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _carve(stream, dtype, device, *shapes):
+    """Dense 1-D or 2-D buffers out of one allocation (4-byte types; each starts
+    on 256 bytes): for a call whose outputs live and die together, an
+    allocation apiece costs more time than its kernel."""
+    at, places = 0, []
+    for shape in shapes:
+        places.append((shape, (shape[1], 1) if len(shape) == 2 else (1,), at))
+        at += (math.prod(shape) + 63) // 64 * 64
+    base = _empty(stream, (at,), dtype=dtype, device=device)
+    return [base.as_strided(*p) for p in places]
+
+
+# Workspaces up to this size are carved out of the outputs' allocation, which
+# they then share the life of.
+_SMALL = 1 << 16
+
+
 def _ptr(t):
-    return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
+    return t.data_ptr() if t is not None else None
 
 
 def _dev(t, name, dtypes):
@@ -506,12 +524,13 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
         _shaped(bias, "bias", (torch.float32,), (E,), dev)
     if mask is not None:
         _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
-    ids = _empty(stream, (T, top_k), dtype=torch.int32, device=dev)
-    weights = _empty(stream, (T, top_k), dtype=torch.float32, device=dev)
-    lse = _empty(stream, (T,), dtype=torch.float32, device=dev)
-    counts = _empty(stream, (E + 1,), dtype=torch.int32, device=dev)
-    loss = _empty(stream, (1,), dtype=torch.float32, device=dev)
-    workspace = _scratch(bsq_moe_route_workspace_size(T, E), workspace, dev, stream)
+    need = bsq_moe_route_workspace_size(T, E)
+    weights, lse, loss = _carve(stream, torch.float32, dev, (T, top_k), (T,), (1,))
+    if workspace is None and need <= _SMALL:
+        ids, counts, workspace = _carve(stream, torch.int32, dev, (T, top_k), (E + 1,), (need // 4,))
+    else:
+        ids, counts = _carve(stream, torch.int32, dev, (T, top_k), (E + 1,))
+        workspace = _scratch(need, workspace, dev, stream)
     _check("bsq_moe_route",
            _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
                               scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss),
@@ -560,10 +579,13 @@ def bsq_moe_dispatch(expert_ids, num_experts, workspace=None, stream=None):
         raise ValueError("expert_ids must be contiguous [tokens, top_k]")
     T, K = expert_ids.shape
     dev = expert_ids.device
-    offsets = _empty(stream, (num_experts + 1,), dtype=torch.int32, device=dev)
-    row_index = _empty(stream, (T * K,), dtype=torch.int32, device=dev)
-    slot = _empty(stream, (T, K), dtype=torch.int32, device=dev)
-    workspace = _scratch(bsq_moe_dispatch_workspace_size(T, K, num_experts), workspace, dev, stream)
+    need = bsq_moe_dispatch_workspace_size(T, K, num_experts)
+    shapes = (num_experts + 1,), (T * K,), (T, K)
+    if workspace is None and need <= _SMALL:
+        offsets, row_index, slot, workspace = _carve(stream, torch.int32, dev, *shapes, (need // 4,))
+    else:
+        offsets, row_index, slot = _carve(stream, torch.int32, dev, *shapes)
+        workspace = _scratch(need, workspace, dev, stream)
     _check("bsq_moe_dispatch",
            _lib.bsq_moe_dispatch(_ptr(expert_ids), T, K, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot),
                                  _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
