@@ -1,9 +1,9 @@
 // Helpers shared by the router, dispatch and combine kernels (gfx950).
 //
-// Wave-wide reductions run on the data-parallel-primitive lane shifts (a
-// shift within rows of 16, then row broadcasts): six VALU instructions whose
-// order is fixed, so a sum is the same in every run.  The result is read from
-// lane 63 into a scalar register.
+// Wave-wide reductions run on the data-parallel-primitive lane moves: four
+// rotations within rows of 16, each one instruction with its operation, then
+// the swaps of 16 and of 32 lanes.  Every lane ends with the result, in an
+// order that is the same in every run.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -13,33 +13,79 @@
 
 namespace bsq {
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ float dpp_f32(float old, float x) {
-    return __int_as_float(__builtin_amdgcn_update_dpp(__float_as_int(old), __float_as_int(x), CTRL, ROWS, 0xF, false));
+// One step of a row's rotation: op(x, x rotated by N lanes), the two wait
+// states between the write of x and its move included.
+#define BSQ_DPP_STEP(NAME, INSTR, T)                                                                         \
+    template <int N>                                                                                         \
+    __device__ __forceinline__ T NAME(T x) {                                                                 \
+        T r;                                                                                                 \
+        asm("s_nop 1\n\t" INSTR " %0, %1, %1 row_ror:%2 row_mask:0xf bank_mask:0xf" : "=v"(r) : "v"(x), "n"(N)); \
+        return r;                                                                                            \
+    }
+BSQ_DPP_STEP(ror_max_f32, "v_max_f32_dpp", float)
+BSQ_DPP_STEP(ror_add_f32, "v_add_f32_dpp", float)
+BSQ_DPP_STEP(ror_max_i32, "v_max_i32_dpp", int)
+#undef BSQ_DPP_STEP
+
+// x of the lane 16 (32) away within each 32 (64), with the lane's own: {x, y} in
+// either order.
+struct Pair32 {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Pair32 swap16(uint32_t x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return {r[0], r[1]};
+}
+__device__ __forceinline__ Pair32 swap32(uint32_t x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return {r[0], r[1]};
 }
 
-__device__ __forceinline__ float lane63(float x) {
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+// fmaxf of values that are no NaN (without the quieting that fmaxf adds).
+__device__ __forceinline__ float max_num(float a, float b) {
+    float r;
+    asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+    return r;
 }
 
 __device__ __forceinline__ float wave_max_f32(float x) {
-    x = fmaxf(x, dpp_f32<0x111, 0xF>(x, x));
-    x = fmaxf(x, dpp_f32<0x112, 0xF>(x, x));
-    x = fmaxf(x, dpp_f32<0x114, 0xF>(x, x));
-    x = fmaxf(x, dpp_f32<0x118, 0xF>(x, x));
-    x = fmaxf(x, dpp_f32<0x142, 0xA>(x, x));
-    x = fmaxf(x, dpp_f32<0x143, 0xC>(x, x));
-    return lane63(x);
+    x = ror_max_f32<1>(ror_max_f32<2>(ror_max_f32<4>(ror_max_f32<8>(x))));
+    Pair32 p = swap16(__float_as_uint(x));
+    x = max_num(__uint_as_float(p.a), __uint_as_float(p.b));
+    p = swap32(__float_as_uint(x));
+    return max_num(__uint_as_float(p.a), __uint_as_float(p.b));
+}
+
+// Sum of the lane's row of 16.
+__device__ __forceinline__ float row_sum_f32(float x) {
+    return ror_add_f32<1>(ror_add_f32<2>(ror_add_f32<4>(ror_add_f32<8>(x))));
 }
 
 __device__ __forceinline__ float wave_sum_f32(float x) {
-    x += dpp_f32<0x111, 0xF>(0.0f, x);
-    x += dpp_f32<0x112, 0xF>(0.0f, x);
-    x += dpp_f32<0x114, 0xF>(0.0f, x);
-    x += dpp_f32<0x118, 0xF>(0.0f, x);
-    x += dpp_f32<0x142, 0xA>(0.0f, x);
-    x += dpp_f32<0x143, 0xC>(0.0f, x);
-    return lane63(x);
+    x = row_sum_f32(x);
+    Pair32 p = swap16(__float_as_uint(x));
+    x = __uint_as_float(p.a) + __uint_as_float(p.b);
+    p = swap32(__float_as_uint(x));
+    return __uint_as_float(p.a) + __uint_as_float(p.b);
+}
+
+__device__ __forceinline__ int wave_max_i32(int x) {
+    x = ror_max_i32<1>(ror_max_i32<2>(ror_max_i32<4>(ror_max_i32<8>(x))));
+    Pair32 p = swap16((uint32_t)x);
+    x = max((int)p.a, (int)p.b);
+    p = swap32((uint32_t)x);
+    return max((int)p.a, (int)p.b);
+}
+
+// e^x for x <= 0 from the hardware's 2^y: x log2(e) in two binary32 parts, the
+// second one applied to first order, so the error stays at about 2 ulps for
+// any x; results below the normal range are 0.
+__device__ __forceinline__ float exp_neg(float x) {
+    x = max_num(x, -200.0f);  // (0 from -104 on; -inf has no remainder)
+    const float y = x * 1.44269502f;  // log2(e) = 1.44269502 + 1.92596e-8
+    const float lo = fmaf(x, 1.92596303e-8f, fmaf(x, 1.44269502f, -y));
+    const float r = __builtin_amdgcn_exp2f(y);
+    return fmaf(r, lo * 0.693147182f, r);
 }
 
 // Inclusive prefix sum over the wave's lanes.

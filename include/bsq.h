@@ -405,8 +405,8 @@ bsq_status bsq_grouped_gemm_w4a16(const void* x_bf16, const uint8_t* w_codes, co
  *   descending order, ties to the lowest index.  NaN counts as -inf and +inf
  *   as the largest finite value; an expert whose key is -inf is never chosen.
  *   A token with fewer than top_k such experts gets id -1 and weight 0 in the
- *   places left, and one with none (or whose mask byte is 0, then its logits
- *   are not read) routes nowhere: lse -inf.
+ *   places left, and one with none (or whose mask byte is 0, whatever its
+ *   logits hold) routes nowhere: lse -inf.
  *   p = softmax(l), lse = log sum_e exp(l_e).  weights = scale * p of the
  *   chosen experts, or with `normalize` scale * (softmax over the chosen).
  * With f_e the tokens that chose e, V the tokens that chose any and P_e =
