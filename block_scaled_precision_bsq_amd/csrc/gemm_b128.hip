@@ -291,7 +291,6 @@ constexpr int WIDE_X = 12;  // MFMAs before a stage's end at which the slot's re
 constexpr int WIDE_Y = 8;   // and at which the next stage is needed (barrier Y)
 constexpr int WIDE_DMA = 9;  // DMA instructions per wave and stage
 constexpr int WIDE_SPREAD = 18;  // MFMAs over which they go out (half as many in the half-height loop)
-constexpr int64_t WIDE_MIN_TILES = 512;
 
 // DMA instruction n of a stage goes out behind the wide_due(n)th MFMA after X
 // (counted through to the next stage); wide_sent(m): how many go before the mth.
@@ -550,6 +549,96 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     else body(IC<4>{});
 }
 
+// A row or two an expert: the weights' bytes bound the product, so they go from
+// memory straight to the registers of the one wave that uses them.  A workgroup
+// takes 16 rows of an expert and 64 columns; its four waves take every fourth
+// block of the reduction, each with the next THIN_DEPTH ones' operands in flight,
+// and add up in LDS in wave order.  64 rows over 32 experts (26 with rows) of
+// 4096 x 7168: 133 us, 5.8 TB/s; non-temporal weight loads 156 us.
+constexpr int TR = 16, TC = 64;
+constexpr int THIN_DEPTH = 2;  // (1 the same, 4: 139 us in the case below)
+template <bool OUT_F32>
+__global__ __launch_bounds__(256, 2) void k_gemm_b128_thin(B128Args p) {
+    __shared__ __align__(16) float4v s_sum[4][4][64];  // [wave][column group][lane]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int CT = (int)((p.C + TC - 1) / TC);
+    const RowTile f = find_row_tile<TR>(p, blockIdx.x / CT, lane);
+    if (f.e < 0) return;
+    const int e = f.e, c0 = TC * (int)(blockIdx.x % CT);
+    const int rows = __builtin_amdgcn_readfirstlane((int)min((int64_t)TR, f.end - f.row0));
+    const int cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)TC, p.C - c0));
+    const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)p.R), M = __builtin_amdgcn_readfirstlane((uint32_t)p.M);
+    const uint32_t len = e < p.E ? ld : 0u;
+    const int nb = (int)((len + 127) / 128);
+    const int64_t we = e < p.E ? e : 0;
+    const float* bs = uniform_ptr(p.bs + we * p.bs_e + (int64_t)(c0 / 128) * p.bs_c);
+    const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(p.a + f.row0 * p.R), (uint32_t)rows * ld);
+    const __amdgpu_buffer_rsrc_t rb = rsrc_n(uniform_ptr(p.b + (we * p.C + c0) * p.R), (uint32_t)cols * ld);
+    const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(p.as + f.row0), 0x7FFFFFFFu);
+    const int lr = lane & 15, q = lane >> 4;
+    const uint32_t at = (uint32_t)lr * ld;
+    struct Stage {
+        u32x4 a[2], b[4][2];
+        float sa, sw;
+    };
+    auto load = [&](Stage& s, int blk) {
+        const uint32_t k0 = 128u * (uint32_t)blk + 16u * (uint32_t)q, k1 = k0 + 64u;
+        const uint32_t o0 = k0 < len ? at + k0 : OOB, o1 = k1 < len ? at + k1 : OOB;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(o0 + (uint32_t)(16 * j) * ld), 0, 0);
+            s.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(o1 + (uint32_t)(16 * j) * ld), 0, 0);
+        }
+        s.a[0] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)o0, 0, 0);
+        s.a[1] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)o1, 0, 0);
+        s.sa = __uint_as_float(buf_load4(rsa, lr < (blk < nb ? rows : 0) ? 4u * ((uint32_t)blk * M + (uint32_t)lr) : OOB));
+        s.sw = bs[(blk < nb ? blk : 0) * p.bs_b];
+    };
+    auto frag = [](const u32x4& x, const u32x4& y) {
+        return int8v{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+    };
+    float4v acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+    auto use = [&](const Stage& s) {
+        const int8v fa = frag(s.a[0], s.a[1]);
+        const float sc = s.sa * s.sw;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4v d = b128_mfma(frag(s.b[j][0], s.b[j][1]), fa);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(d[v], sc, acc[j][v]);
+        }
+    };
+    Stage s[THIN_DEPTH];
+    if (nb > 0) {
+#pragma unroll
+        for (int i = 0; i < THIN_DEPTH; ++i) load(s[i], wave + 4 * i);
+        for (int blk = wave; blk < nb; blk += 4 * THIN_DEPTH) {
+#pragma unroll
+            for (int i = 0; i < THIN_DEPTH; ++i) {
+                use(s[i]);  // zeros past the last block
+                load(s[i], blk + 4 * (THIN_DEPTH + i));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s_sum[wave][j][lane] = acc[j];
+    __syncthreads();
+    float4v r = s_sum[0][wave][lane];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) r += s_sum[w][wave][lane];
+    const __amdgpu_buffer_rsrc_t ro = make_rsrc(
+        uniform_ptr(static_cast<char*>(p.out) + (f.row0 * p.C + c0) * (OUT_F32 ? 4 : 2)), 0x7FFFFFFFu);
+    const int c = 16 * wave + 4 * q;
+    const uint32_t o = (lr < rows && c < cols) ? ((uint32_t)lr * (uint32_t)p.C + (uint32_t)c) * (OUT_F32 ? 4u : 2u) : OOB;
+    if constexpr (OUT_F32)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, r), ro, (int)o, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])}, ro, (int)o, 0, 0);
+}
+
 namespace {
 
 constexpr int64_t kMaxOffset = (int64_t)1 << 31;  // 32-bit buffer offsets
@@ -559,10 +648,28 @@ bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (
 // Most row tiles of TM rows that E experts and the rows past them can need.
 int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M : E + 1); }
 
+// Which form runs, by the call's sizes:
+//  - at most THIN_ROWS rows an expert on average (not wgrad): 16 x 64 tiles.  32
+//    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles
+//    and 192 of the 128 x 128 ones, 128 rows 165 against 160 and 204.
+//  - 128 x 128 tiles while all of them run at once, two to a compute unit: 3001
+//    rows, 12 experts of 1424 x 2000 30 us against 34 of the 256 x 256 tiles;
+//    one round more, 4096 rows and 1 expert of 4096 x 4096, 92 against 60.
+//  - else 256 x 256 tiles.
+constexpr int64_t THIN_ROWS = 2;
+constexpr int64_t TILES_AT_ONCE = 512;
+
+template <class K>
+bsq_status run(K kernel, int64_t grid, int threads, size_t lds, const B128Args& a, hipStream_t s) {
+    if (grid * threads >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, s, a);
+    return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
+}
+
 template <bool F32, bool WGRAD>
-bsq_status launch_wide(const B128Args& a, int64_t tiles, hipStream_t s) {
-    const int64_t grid = (tiles + 255) / 256 * 256;
-    if (grid * 512 >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
+bsq_status launch_wide(const B128Args& a, hipStream_t s) {
+    const int64_t ct = (a.C + WT - 1) / WT;
+    const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + WT - 1) / WT) * ct : (max_row_tiles(a.M, a.E, WT) + 3) / 4 * 4 * ct;
     static bool attr_set = false;  // idempotent; racing writers set the same value
     if (!attr_set) {
         if (hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_b128_wide<F32, WGRAD>),
@@ -570,31 +677,24 @@ bsq_status launch_wide(const B128Args& a, int64_t tiles, hipStream_t s) {
             return BSQ_ERR_HIP;
         attr_set = true;
     }
-    hipLaunchKernelGGL((k_gemm_b128_wide<F32, WGRAD>), dim3((unsigned)grid), dim3(512), 2 * WIDE_SLOT, s, a);
-    return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
+    return run(k_gemm_b128_wide<F32, WGRAD>, (tiles + 255) / 256 * 256, 512, 2 * WIDE_SLOT, a, s);
+}
+
+template <bool F32, bool WGRAD>
+bsq_status launch_b128(const B128Args& a, hipStream_t s) {
+    if constexpr (!WGRAD)
+        if (a.M <= THIN_ROWS * a.E)
+            return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
+    const int64_t ct = (a.C + BT - 1) / BT;
+    const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : max_row_tiles(a.M, a.E, BT) * ct;
+    if (tiles > TILES_AT_ONCE) return launch_wide<F32, WGRAD>(a, s);
+    // (row tiles in groups of 8)
+    return run(k_gemm_b128_tile<F32, WGRAD>, WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct, 256, 0, a, s);
 }
 
 template <bool WGRAD>
 bsq_status launch_b128(const B128Args& a, bool f32, hipStream_t s) {
-    {
-        const int64_t wct = (a.C + WT - 1) / WT;
-        const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + WT - 1) / WT) * wct
-                                    : (max_row_tiles(a.M, a.E, WT) + 3) / 4 * 4 * wct;
-        if (tiles >= WIDE_MIN_TILES)
-            return f32 ? launch_wide<true, WGRAD>(a, tiles, s) : launch_wide<false, WGRAD>(a, tiles, s);
-    }
-    const int64_t ct = (a.C + BT - 1) / BT;
-    int64_t grid;
-    if (WGRAD)
-        grid = (int64_t)a.E * ((a.R + BT - 1) / BT) * ct;
-    else
-        grid = (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;
-    if (grid * 256 >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
-    if (f32)
-        hipLaunchKernelGGL((k_gemm_b128_tile<true, WGRAD>), dim3((unsigned)grid), dim3(256), 0, s, a);
-    else
-        hipLaunchKernelGGL((k_gemm_b128_tile<false, WGRAD>), dim3((unsigned)grid), dim3(256), 0, s, a);
-    return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
+    return f32 ? launch_b128<true, WGRAD>(a, s) : launch_b128<false, WGRAD>(a, s);
 }
 
 }  // namespace

@@ -521,7 +521,7 @@ bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts,
  *   y[m][j] = sum_b a_scale[b][m] w_scale[e][j/128][b] sum_{k in block b} a[m][k] w_e[j][k]
  * for every row m of expert e's segment (num_experts == 1: a plain product).
  * A block's 128 products are summed by the matrix core, the blocks in binary32
- * in ascending order.  Rows past offsets[num_experts] become zero.
+ * in an order that depends on the call's sizes only.  Rows past offsets[num_experts] become zero.
  *   a_codes [m_total][k], w_codes [E*n][k] 16-byte aligned; n % 16 == 0,
  *   k % 16 == 0; y [m_total][n] in y_dtype.
  *
