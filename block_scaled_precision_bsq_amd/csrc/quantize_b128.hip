@@ -5,10 +5,12 @@
 //
 // A block with maximum magnitude a: c = max(a, 2^-100), code of x =
 // E4M3_RNE(RN(x * RN(448 / c))) (saturating: the product may round past 448),
-// scale = RN(c / 448), and 0 for an all-zero block.  The two divisions are the
-// IEEE ones, once per block; an element costs one multiply, one clamp and its
-// share of a packed conversion, so every kernel here is bound by its bytes:
-// 2 per element read, 1 or 2 written.
+// scale = RN(c / 448), and 0 for an all-zero block.  The two divisions are
+// correctly rounded, once per block; an element costs an unpack, a multiply and
+// its share of a packed conversion.  The product is below 448 (1 + 2^-23), which
+// rounds to 448, so there is no clamp.  With few enough instructions around
+// them every kernel here is bound by its bytes: 2 per element read, 1 or 2
+// written.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -22,28 +24,71 @@ constexpr float B128_TINY = 0x1p-100f;
 struct B128Scale {
     float inv, scale;
 };
-// From the maximum's bf16 magnitude bits.
+// From the maximum's bf16 magnitude bits.  A quotient estimate q with its exact
+// remainder r gives RN(q + r y) with y the reciprocal: before the rounding it is
+// within 2^-45 of the true quotient, and a quotient of integers below 2^8
+// (448 = 7 * 64; c has 8 bits) is either a binary32 number or at least 2^-33 away
+// from the middle of two.
 __device__ __forceinline__ B128Scale b128_scale(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits << 16);
     const float c = fmaxf(a, B128_TINY);
-    return {448.0f / c, a > 0.0f ? c / 448.0f : 0.0f};
+    const float y = __builtin_amdgcn_rcpf(c), z = 1.0f / 448.0f;
+    const float q = 448.0f * y, p = c * z;
+    const float inv = fmaf(fmaf(-c, q, 448.0f), y, q);
+    const float scale = fmaf(fmaf(-448.0f, p, c), z, p);
+    return {inv, a > 0.0f ? scale : 0.0f};
+}
+
+// E4M3 bytes of four floats of magnitude below 464, a in the lowest byte.
+__device__ __forceinline__ uint32_t b128_e4m3x4(float a, float b, float c, float d) {
+    return __builtin_amdgcn_cvt_pk_fp8_f32(c, d, __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false), true);
 }
 
 // E4M3 codes of four packed pairs (8 elements) times inv.
 __device__ __forceinline__ uint2 b128_codes8(uint4 w, float inv) {
-    return make_uint2(e4m3x4(bf16_lo(w.x) * inv, bf16_hi(w.x) * inv, bf16_lo(w.y) * inv, bf16_hi(w.y) * inv),
-                      e4m3x4(bf16_lo(w.z) * inv, bf16_hi(w.z) * inv, bf16_lo(w.w) * inv, bf16_hi(w.w) * inv));
+    return make_uint2(b128_e4m3x4(bf16_lo(w.x) * inv, bf16_hi(w.x) * inv, bf16_lo(w.y) * inv, bf16_hi(w.y) * inv),
+                      b128_e4m3x4(bf16_lo(w.z) * inv, bf16_hi(w.z) * inv, bf16_lo(w.w) * inv, bf16_hi(w.w) * inv));
 }
 
 __device__ __forceinline__ uint32_t absmax8(uint4 w) {
     return fold_max16(absmax2_bf16(absmax2_bf16(absmax2_bf16(w.x & 0x7FFF7FFFu, w.y), w.z), w.w));
 }
 
-// Maximum over a group of 16 lanes.
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
+// Lane moves within rows of 16.
+template <int CTRL>
+__device__ __forceinline__ uint32_t row_move(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
+}
+
+// Eight maxima over the 16 lanes of a row, scattered: lane l gets the one of
+// m[l / 2].  Each step halves the values a lane works on: it keeps those of its
+// half and takes the partner's share of them, partners l ^ 8, l ^ 7, l ^ 2, and
+// last adds l ^ 1.
+__device__ __forceinline__ uint32_t scatter_max16(const uint32_t (&m)[8], int l) {
+    uint32_t a[4], b[2];
 #pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, off, 16));
-    return v;
+    for (int i = 0; i < 4; ++i) a[i] = max((l & 8) ? m[i + 4] : m[i], row_move<0x128>((l & 8) ? m[i] : m[i + 4]));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) b[i] = max((l & 4) ? a[i + 2] : a[i], row_move<0x141>((l & 4) ? a[i] : a[i + 2]));
+    const uint32_t c = max((l & 2) ? b[1] : b[0], row_move<0x4E>((l & 2) ? b[0] : b[1]));
+    return max(c, row_move<0xB1>(c));
+}
+// The value that lane 2 I of the row holds.
+template <int I>
+__device__ __forceinline__ float row_value(float x) { return __uint_as_float(row_move<0x150 + 2 * I>(__float_as_uint(x))); }
+
+// Codes of eight pieces of 8 elements, the inverse of piece i in lane 2 i of
+// the row; store(i, codes) takes them.
+template <class F>
+__device__ __forceinline__ void codes_of_row(const uint4 (&w)[8], float inv, F store) {
+    store(0, b128_codes8(w[0], row_value<0>(inv)));
+    store(1, b128_codes8(w[1], row_value<1>(inv)));
+    store(2, b128_codes8(w[2], row_value<2>(inv)));
+    store(3, b128_codes8(w[3], row_value<3>(inv)));
+    store(4, b128_codes8(w[4], row_value<4>(inv)));
+    store(5, b128_codes8(w[5], row_value<5>(inv)));
+    store(6, b128_codes8(w[6], row_value<6>(inv)));
+    store(7, b128_codes8(w[7], row_value<7>(inv)));
 }
 
 // Rows.  Sixteen lanes take a block (8 elements, 16 bytes each), a workgroup
@@ -73,13 +118,15 @@ __global__ __launch_bounds__(256) void k_quantize_b128_rows(const uint16_t* __re
         w[b] = make_uint4(0, 0, 0, 0);
         if (src >= 0 && c < cols) w[b] = *reinterpret_cast<const uint4*>(x + src * ld + c);
     }
+    uint32_t m[ROWS_B];
 #pragma unroll
-    for (int b = 0; b < ROWS_B; ++b) {
+    for (int b = 0; b < ROWS_B; ++b) m[b] = absmax8(w[b]);
+    const B128Scale q = b128_scale(scatter_max16(m, l));
+    if ((l & 1) == 0) s_scale[l >> 1][g] = q.scale;
+    codes_of_row(w, q.inv, [&](int b, uint2 v) {
         const int c = 128 * (b0 + b) + 8 * l;
-        const B128Scale q = b128_scale(max16(absmax8(w[b])));
-        if (l == 0) s_scale[b][g] = q.scale;
-        if (r < rows && c < cols) *reinterpret_cast<uint2*>(codes + r * cols + c) = b128_codes8(w[b], q.inv);
-    }
+        if (r < rows && c < cols) *reinterpret_cast<uint2*>(codes + r * cols + c) = v;
+    });
     __syncthreads();
     const int b = threadIdx.x >> 4;
     const int64_t rr = (int64_t)blockIdx.x * ROWS_R + l;
@@ -105,7 +152,7 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
                                                             float* __restrict__ scale, uint8_t* __restrict__ t_codes,
                                                             float* __restrict__ t_scale) {
     __shared__ __align__(16) uint8_t s_x[128 * 256];
-    __shared__ uint32_t s_max[4][128];
+    __shared__ uint32_t s_max[4][64];  // two 16-bit magnitudes
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t blk = blockIdx.y;
     const int c0 = blockIdx.x * 128;
@@ -124,77 +171,97 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
     }
     const bool tail = grp == G;
     const int64_t o0 = offsets[grp], o1 = tail ? rows : min((int64_t)offsets[grp + 1], rows);
-    const int64_t first = o0 + 128 * (blk - grp - max((int64_t)0, o0) / 128);
-    const int nr = (o0 >= 0 && first >= o0) ? (int)max((int64_t)0, min((int64_t)128, o1 - first)) : 0;
+    const int64_t first = uniform_i64(o0 + 128 * (blk - grp - max((int64_t)0, o0) / 128));
+    const int nr = __builtin_amdgcn_readfirstlane(
+        (o0 >= 0 && first >= o0) ? (int)max((int64_t)0, min((int64_t)128, o1 - first)) : 0);
 
     // load: 16 threads a row, 8 steps of 16 rows
     const bool need = ROWS || !tail;
     const int ch = tid & 15, rg = tid >> 4;
     uint4 w[8];
+    if constexpr (GATHER) {
+        const uint16_t* xc = x + c0 + 8 * ch;
+        const int limit = (need && 8 * ch < nc) ? nr : 0;
+        int32_t src[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int r = 16 * i + rg;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (need && r < nr && 8 * ch < nc) {
-            int64_t src = first + r;
-            if (GATHER) {
-                const int32_t k = row_index[src];
-                src = (uint32_t)k < (uint64_t)src_rows ? k : -1;
-            }
-            if (src >= 0) w[i] = *reinterpret_cast<const uint4*>(x + src * ld + c0 + 8 * ch);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(s_x + tile_at(16 * i + rg, ch)) = w[i];
-    if (ROWS) {
-        // the rows' own codes: 16 threads hold one row's block
+        for (int i = 0; i < 8; ++i) src[i] = 16 * i + rg < limit ? row_index[first + 16 * i + rg] : -1;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = 16 * i + rg;
-            const B128Scale q = b128_scale(max16(absmax8(w[i])));
-            if (r < nr) {
-                if (8 * ch < nc)
-                    *reinterpret_cast<uint2*>(codes + (first + r) * cols + c0 + 8 * ch) = b128_codes8(w[i], q.inv);
-                if (ch == 0) scale[(int64_t)blockIdx.x * rows + first + r] = q.scale;
-            }
+            w[i] = make_uint4(0, 0, 0, 0);
+            if ((uint32_t)src[i] < (uint32_t)src_rows)
+                w[i] = *reinterpret_cast<const uint4*>(xc + (uint64_t)(uint32_t)src[i] * (uint32_t)ld);
         }
+    } else {
+        // rows past the tile lie past the resource's range
+        const __amdgpu_buffer_rsrc_t rx =
+            make_rsrc(uniform_ptr(x + first * ld + c0), (need && nr > 0) ? 2u * ((uint32_t)(nr - 1) * (uint32_t)ld + (uint32_t)nc) : 0u);
+        const uint32_t o = 8 * ch < nc ? 2u * ((uint32_t)rg * (uint32_t)ld + 8u * (uint32_t)ch) : OOB;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = buf_load16(rx, o + (uint32_t)(32 * i) * (uint32_t)ld);
+    }
+    const uint32_t put = tile_at(rg, ch);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(s_x + put + 4096u * i) = w[i];
+    if (ROWS) {
+        // the rows' own codes: 16 threads hold one row's block
+        uint32_t m[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = absmax8(w[i]);
+        const B128Scale q = b128_scale(scatter_max16(m, ch));
+        const int mine = 16 * (ch >> 1) + rg;  // the row whose scale this lane has
+        if ((ch & 1) == 0 && mine < nr) scale[(int64_t)blockIdx.x * rows + first + mine] = q.scale;
+        const __amdgpu_buffer_rsrc_t rc = make_rsrc(uniform_ptr(codes + first * cols + c0),
+                                                    nr > 0 ? (uint32_t)(nr - 1) * (uint32_t)cols + (uint32_t)nc : 0u);
+        const uint32_t o = 8 * ch < nc ? (uint32_t)rg * (uint32_t)cols + 8u * (uint32_t)ch : OOB;
+        codes_of_row(w, q.inv, [&](int i, uint2 v) {
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, rc, (int)(o + (uint32_t)(16 * i) * (uint32_t)cols), 0, 0);
+        });
+    }
+    // columns past the tile lie past the resource's range
+    const __amdgpu_buffer_rsrc_t rt = make_rsrc(uniform_ptr(t_codes + (int64_t)c0 * P + 128 * blk), (uint32_t)(nc - 1) * (uint32_t)P + 128u);
+    const uint32_t to = (uint32_t)(tid >> 3) * (uint32_t)P + 16u * (uint32_t)(tid & 7);
+    if (tail || nr == 0) {
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b128(zero, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, 0);
+        if (tid < nc) t_scale[blk * cols + c0 + tid] = 0.0f;
+        return;
     }
     __syncthreads();
     // columns (the transposed codes go where the tile was once every thread
     // holds its share in registers): thread (p, q) takes channels 2p, 2p + 1 and rows 32q ..
     const int p = tid & 63, q = tid >> 6;
     uint32_t v[32], m = 0;
+    const uint32_t get = (uint32_t)(8192 * q + 16 * (p >> 2) + 4 * (p & 3));  // tile_at(32 q, p / 4)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        v[i] = *reinterpret_cast<const uint32_t*>(s_x + tile_at(32 * q + i, p >> 2) + 4 * (p & 3));
-        if (ROWS && tail) v[i] = 0;
-        m = absmax2_bf16(m, v[i]);
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t at = get ^ (uint32_t)(16 * i);
+        v[i] = *reinterpret_cast<const uint32_t*>(s_x + at + 256 * i);
+        v[i + 16] = *reinterpret_cast<const uint32_t*>(s_x + at + 256 * (i + 16));
     }
-    s_max[q][2 * p] = m & 0xFFFFu;
-    s_max[q][2 * p + 1] = m >> 16;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = absmax2_bf16(m, v[i]);
+    *reinterpret_cast<uint32_t*>(&s_max[q][p]) = m;
     __syncthreads();
-    const B128Scale a = b128_scale(max(max(s_max[0][2 * p], s_max[1][2 * p]), max(s_max[2][2 * p], s_max[3][2 * p])));
-    const B128Scale b = b128_scale(
-        max(max(s_max[0][2 * p + 1], s_max[1][2 * p + 1]), max(s_max[2][2 * p + 1], s_max[3][2 * p + 1])));
+    m = absmax2_bf16(absmax2_bf16(s_max[0][p], s_max[1][p]), absmax2_bf16(s_max[2][p], s_max[3][p]));
+    const B128Scale a = b128_scale(m & 0xFFFFu), b = b128_scale(m >> 16);
     if (q == 0 && 2 * p < nc) {
         t_scale[blk * cols + c0 + 2 * p] = a.scale;
         t_scale[blk * cols + c0 + 2 * p + 1] = b.scale;
     }
+    uint32_t* ta = reinterpret_cast<uint32_t*>(s_x + TILE_T * (2 * p) + 32 * q);
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-        *reinterpret_cast<uint32_t*>(s_x + TILE_T * (2 * p) + 32 * q + i) =
-            e4m3x4(bf16_lo(v[i]) * a.inv, bf16_lo(v[i + 1]) * a.inv, bf16_lo(v[i + 2]) * a.inv, bf16_lo(v[i + 3]) * a.inv);
-        *reinterpret_cast<uint32_t*>(s_x + TILE_T * (2 * p + 1) + 32 * q + i) =
-            e4m3x4(bf16_hi(v[i]) * b.inv, bf16_hi(v[i + 1]) * b.inv, bf16_hi(v[i + 2]) * b.inv, bf16_hi(v[i + 3]) * b.inv);
+        ta[i / 4] = b128_e4m3x4(bf16_lo(v[i]) * a.inv, bf16_lo(v[i + 1]) * a.inv, bf16_lo(v[i + 2]) * a.inv, bf16_lo(v[i + 3]) * a.inv);
+        ta[TILE_T / 4 + i / 4] =
+            b128_e4m3x4(bf16_hi(v[i]) * b.inv, bf16_hi(v[i + 1]) * b.inv, bf16_hi(v[i + 2]) * b.inv, bf16_hi(v[i + 3]) * b.inv);
     }
     __syncthreads();
+    const uint32_t* ts = reinterpret_cast<const uint32_t*>(s_x + TILE_T * (tid >> 3) + 16 * (tid & 7));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int c = 32 * i + (tid >> 3), k = tid & 7;
-        const uint32_t* s = reinterpret_cast<const uint32_t*>(s_x + TILE_T * c + 16 * k);
-        if (c < nc)
-            *reinterpret_cast<uint4*>(t_codes + (int64_t)(c0 + c) * P + 128 * blk + 16 * k) =
-                make_uint4(s[0], s[1], s[2], s[3]);
+        const uint32_t* c = ts + 32 * i * (TILE_T / 4);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[0], c[1], c[2], c[3]}, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, 0);
     }
 }
 
@@ -290,7 +357,7 @@ bsq_status bsq_quantize_fp8b128(const void* x_bf16, int64_t src_rows, int64_t co
     const int64_t P = bsq_colwise_padded_cols(num_groups, rows);
     if (cols > ((int64_t)1 << 22) || src_rows >= (int64_t)1 << 31 || rows > ((int64_t)1 << 27)) return BSQ_ERR_UNSUPPORTED;
     const uint16_t* x = static_cast<const uint16_t*>(x_bf16);
-    if (t_codes && P / 128 > 65535) return BSQ_ERR_UNSUPPORTED;
+    if (t_codes && (P / 128 > 65535 || ld_x >= (int64_t)1 << 23)) return BSQ_ERR_UNSUPPORTED;  // 32-bit offsets in a tile
     if (!t_codes) {
         const dim3 grid((unsigned)((rows + bsq::ROWS_R - 1) / bsq::ROWS_R),
                         (unsigned)((cols + 128 * bsq::ROWS_B - 1) / (128 * bsq::ROWS_B)));
