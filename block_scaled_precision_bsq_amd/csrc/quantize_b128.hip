@@ -20,6 +20,10 @@
 namespace bsq {
 
 constexpr float B128_TINY = 0x1p-100f;
+// Cache policy of the code stores: non-temporal.  They are whole 128-byte lines
+// that the kernel does not read (with ordinary stores 137 us instead of 117 for
+// 4096 tokens gathered into 32768 x 7168 row and column codes, 5.8 TB/s).
+constexpr int NT = 2;
 
 struct B128Scale {
     float inv, scale;
@@ -214,7 +218,7 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
                                                     nr > 0 ? (uint32_t)(nr - 1) * (uint32_t)cols + (uint32_t)nc : 0u);
         const uint32_t o = 8 * ch < nc ? (uint32_t)rg * (uint32_t)cols + 8u * (uint32_t)ch : OOB;
         codes_of_row(w, q.inv, [&](int i, uint2 v) {
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, rc, (int)(o + (uint32_t)(16 * i) * (uint32_t)cols), 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{v.x, v.y}, rc, (int)(o + (uint32_t)(16 * i) * (uint32_t)cols), 0, NT);
         });
     }
     // columns past the tile lie past the resource's range
@@ -223,7 +227,7 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
     if (tail || nr == 0) {
         const u32x4 zero = {0, 0, 0, 0};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b128(zero, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, 0);
+        for (int i = 0; i < 4; ++i) __builtin_amdgcn_raw_buffer_store_b128(zero, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, NT);
         if (tid < nc) t_scale[blk * cols + c0 + tid] = 0.0f;
         return;
     }
@@ -261,11 +265,12 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t* c = ts + 32 * i * (TILE_T / 4);
-        __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[0], c[1], c[2], c[3]}, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{c[0], c[1], c[2], c[3]}, rt, (int)(to + (uint32_t)(32 * i) * (uint32_t)P), 0, NT);
     }
 }
 
-// Weights: one workgroup per 128 x 128 block of one expert.
+// Weights: one workgroup per 128 x 128 block of one expert.  32 x 4096 x 7168:
+// 674 us, 5.6 TB/s, the copy rate (ordinary loads and stores 696 us).
 template <bool TRANS>
 __global__ __launch_bounds__(256) void k_quantize_b128_weights(const uint16_t* __restrict__ w, int n, int k,
                                                                int64_t ld, uint8_t* __restrict__ codes,
@@ -284,7 +289,7 @@ __global__ __launch_bounds__(256) void k_quantize_b128_weights(const uint16_t* _
     for (int i = 0; i < 8; ++i) {
         const int r = 16 * i + rg;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (r < nr && 8 * ch < nc) v[i] = *reinterpret_cast<const uint4*>(w + (e * n + n0 + r) * ld + k0 + 8 * ch);
+        if (r < nr && 8 * ch < nc) v[i] = ld_stream16(w + (e * n + n0 + r) * ld + k0 + 8 * ch);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, absmax8(v[i]));
@@ -297,7 +302,7 @@ __global__ __launch_bounds__(256) void k_quantize_b128_weights(const uint16_t* _
     for (int i = 0; i < 8; ++i) {
         const int r = 16 * i + rg;
         const uint2 c = b128_codes8(v[i], q.inv);
-        if (r < nr && 8 * ch < nc) *reinterpret_cast<uint2*>(codes + (e * n + n0 + r) * k + k0 + 8 * ch) = c;
+        if (r < nr && 8 * ch < nc) st_stream8(codes + (e * n + n0 + r) * k + k0 + 8 * ch, c);
         if (TRANS) {
             uint32_t* s = reinterpret_cast<uint32_t*>(s_c + TILE_T * r + 8 * ch);
             s[0] = c.x;
@@ -327,8 +332,8 @@ __global__ __launch_bounds__(256) void k_quantize_b128_weights(const uint16_t* _
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 if (4 * cg + j < nc)
-                    *reinterpret_cast<uint4*>(codes_t + (e * k + k0 + 4 * cg + j) * (int64_t)n + n0 + 16 * rq) =
-                        make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]);
+                    st_stream16(codes_t + (e * k + k0 + 4 * cg + j) * (int64_t)n + n0 + 16 * rq,
+                                make_uint4(o[j][0], o[j][1], o[j][2], o[j][3]));
         }
     }
 }
