@@ -10,7 +10,6 @@ importing this package fails if the library has not been built.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 
 import torch
@@ -105,21 +104,27 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _carve(stream, dtype, device, *shapes):
+# Workspaces up to this size come out of the outputs' allocation, which they
+# then share the life of.
+_SMALL = 1 << 16
+
+
+def _carve(stream, dtype, device, shapes, scratch=None):
     """Dense 1-D or 2-D buffers out of one allocation (4-byte types; each starts
     on 256 bytes): for a call whose outputs live and die together, an
-    allocation apiece costs more time than its kernel."""
+    allocation apiece costs more time than its kernel.  With ``scratch`` bytes
+    also the address of that much workspace (last)."""
     at, places = 0, []
     for shape in shapes:
-        places.append((shape, (shape[1], 1) if len(shape) == 2 else (1,), at))
-        at += (math.prod(shape) + 63) // 64 * 64
-    base = _empty(stream, (at,), dtype=dtype, device=device)
-    return [base.as_strided(*p) for p in places]
-
-
-# Workspaces up to this size are carved out of the outputs' allocation, which
-# they then share the life of.
-_SMALL = 1 << 16
+        if len(shape) == 2:
+            places.append((shape, (shape[1], 1), at))
+            at += (shape[0] * shape[1] + 63) // 64 * 64
+        else:
+            places.append((shape, (1,), at))
+            at += (shape[0] + 63) // 64 * 64
+    base = _empty(stream, (at + (scratch or 0) // 4,), dtype, device)
+    out = [base.as_strided(*p) for p in places]
+    return out if scratch is None else out + [base.data_ptr() + 4 * at]
 
 
 def _ptr(t):
@@ -479,7 +484,7 @@ def _dtype_id(t, name):
 def _shaped(t, name, dtypes, shape, dev):
     """Checks a dense input or output buffer."""
     _dev(t, name, dtypes)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != dev:
+    if t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} on {dev}")
     return t
 
@@ -525,16 +530,17 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
     if mask is not None:
         _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
     need = bsq_moe_route_workspace_size(T, E)
-    weights, lse, loss = _carve(stream, torch.float32, dev, (T, top_k), (T,), (1,))
+    weights, lse, loss = _carve(stream, torch.float32, dev, ((T, top_k), (T,), (1,)))
     if workspace is None and need <= _SMALL:
-        ids, counts, workspace = _carve(stream, torch.int32, dev, (T, top_k), (E + 1,), (need // 4,))
+        ids, counts, ws = _carve(stream, torch.int32, dev, ((T, top_k), (E + 1,)), need)
     else:
-        ids, counts = _carve(stream, torch.int32, dev, (T, top_k), (E + 1,))
+        ids, counts = _carve(stream, torch.int32, dev, ((T, top_k), (E + 1,)))
         workspace = _scratch(need, workspace, dev, stream)
+        ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check("bsq_moe_route",
            _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
-                              scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss),
-                              _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+                              scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss), ws, need,
+                              _stream(stream)))
     return ids, weights, lse, counts, loss
 
 
@@ -582,13 +588,14 @@ def bsq_moe_dispatch(expert_ids, num_experts, workspace=None, stream=None):
     need = bsq_moe_dispatch_workspace_size(T, K, num_experts)
     shapes = (num_experts + 1,), (T * K,), (T, K)
     if workspace is None and need <= _SMALL:
-        offsets, row_index, slot, workspace = _carve(stream, torch.int32, dev, *shapes, (need // 4,))
+        offsets, row_index, slot, ws = _carve(stream, torch.int32, dev, shapes, need)
     else:
-        offsets, row_index, slot = _carve(stream, torch.int32, dev, *shapes)
+        offsets, row_index, slot = _carve(stream, torch.int32, dev, shapes)
         workspace = _scratch(need, workspace, dev, stream)
+        ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
     _check("bsq_moe_dispatch",
-           _lib.bsq_moe_dispatch(_ptr(expert_ids), T, K, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot),
-                                 _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+           _lib.bsq_moe_dispatch(_ptr(expert_ids), T, K, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot), ws,
+                                 need, _stream(stream)))
     return offsets, row_index, slot
 
 

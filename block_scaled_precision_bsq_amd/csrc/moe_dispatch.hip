@@ -24,7 +24,9 @@ constexpr int DISPATCH_MAX_E = 1024;
 constexpr int DISPATCH_WAVES = 16;
 constexpr int DISPATCH_ONE_BLOCK = 4096;
 constexpr int DISPATCH_MAX_BLOCKS = 128;
-constexpr int DISPATCH_BLOCK = 2048;  // choices per workgroup while there are workgroups to take them
+// choices per workgroup while there are workgroups to take them (131072 choices:
+// the call 14.4 us; with 2048 or 1024 15.5)
+constexpr int DISPATCH_BLOCK = 4096;
 
 struct DispatchArgs {
     const int32_t* ids;
