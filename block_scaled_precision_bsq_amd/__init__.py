@@ -109,22 +109,17 @@ def _empty(stream, shape, dtype, device):
 _SMALL = 1 << 16
 
 
-def _carve(stream, dtype, device, shapes, scratch=None):
-    """Dense 1-D or 2-D buffers out of one allocation (4-byte types; each starts
-    on 256 bytes): for a call whose outputs live and die together, an
-    allocation apiece costs more time than its kernel.  With ``scratch`` bytes
-    also the address of that much workspace (last)."""
-    at, places = 0, []
-    for shape in shapes:
-        if len(shape) == 2:
-            places.append((shape, (shape[1], 1), at))
-            at += (shape[0] * shape[1] + 63) // 64 * 64
-        else:
-            places.append((shape, (1,), at))
-            at += (shape[0] + 63) // 64 * 64
-    base = _empty(stream, (at + (scratch or 0) // 4,), dtype, device)
-    out = [base.as_strided(*p) for p in places]
-    return out if scratch is None else out + [base.data_ptr() + 4 * at]
+def _carve(stream, dtype, device, sizes, scratch=None):
+    """Dense 1-D buffers of the given lengths out of one allocation (4-byte
+    types): for a call whose outputs live and die together, an allocation
+    apiece costs more time than its kernel.  With ``scratch`` bytes also the
+    address of that much workspace (last), on 256 bytes."""
+    if scratch is None:
+        return _empty(stream, (sum(sizes),), dtype, device).split_with_sizes(sizes)
+    n = sum(sizes)
+    base = _empty(stream, (n + scratch // 4 + 64,), dtype, device)
+    *out, rest = base.split_with_sizes((*sizes, scratch // 4 + 64))
+    return *out, (base.data_ptr() + 4 * n + 255) & -256
 
 
 def _ptr(t):
@@ -530,13 +525,14 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
     if mask is not None:
         _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
     need = bsq_moe_route_workspace_size(T, E)
-    weights, lse, loss = _carve(stream, torch.float32, dev, ((T, top_k), (T,), (1,)))
+    weights, lse, loss = _carve(stream, torch.float32, dev, (T * top_k, T, 1))
     if workspace is None and need <= _SMALL:
-        ids, counts, ws = _carve(stream, torch.int32, dev, ((T, top_k), (E + 1,)), need)
+        ids, counts, ws = _carve(stream, torch.int32, dev, (T * top_k, E + 1), need)
     else:
-        ids, counts = _carve(stream, torch.int32, dev, ((T, top_k), (E + 1,)))
+        ids, counts = _carve(stream, torch.int32, dev, (T * top_k, E + 1))
         workspace = _scratch(need, workspace, dev, stream)
         ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
+    ids, weights = ids.view(T, top_k), weights.view(T, top_k)
     _check("bsq_moe_route",
            _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
                               scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss), ws, need,
@@ -586,13 +582,14 @@ def bsq_moe_dispatch(expert_ids, num_experts, workspace=None, stream=None):
     T, K = expert_ids.shape
     dev = expert_ids.device
     need = bsq_moe_dispatch_workspace_size(T, K, num_experts)
-    shapes = (num_experts + 1,), (T * K,), (T, K)
+    sizes = num_experts + 1, T * K, T * K
     if workspace is None and need <= _SMALL:
-        offsets, row_index, slot, ws = _carve(stream, torch.int32, dev, shapes, need)
+        offsets, row_index, slot, ws = _carve(stream, torch.int32, dev, sizes, need)
     else:
-        offsets, row_index, slot = _carve(stream, torch.int32, dev, shapes)
+        offsets, row_index, slot = _carve(stream, torch.int32, dev, sizes)
         workspace = _scratch(need, workspace, dev, stream)
         ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
+    slot = slot.view(T, K)
     _check("bsq_moe_dispatch",
            _lib.bsq_moe_dispatch(_ptr(expert_ids), T, K, num_experts, _ptr(offsets), _ptr(row_index), _ptr(slot), ws,
                                  need, _stream(stream)))
