@@ -97,7 +97,10 @@ __device__ __forceinline__ RowTile find_row_tile(const B128Args& p, int64_t rt, 
 }
 
 // 128 x 128 output tiles: 4 waves of 64 x 64, a ring of two 128-byte stages
-// per operand filled by buffer-to-LDS DMA, two workgroups per CU.
+// per operand filled by buffer-to-LDS DMA, two workgroups per CU.  A stage's
+// products take a fraction of its loads' latency, so two stages are in flight:
+// 3001 rows over 12 experts of 1424 x 2000 28.9 us (with one 30.3; 12 us are the
+// host's), 1024 rows over 32 experts of 4096 x 7168 197 us (273).
 constexpr int BT = 128;
 struct B128Slot {
     uint8_t a[BT * 128];
@@ -149,14 +152,15 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         r0 = BT * (l % RT);
         c0 = BT * (l / RT);
         rows = (int)min((int64_t)BT, p.R - r0);
-        // the whole call is dropped where any offset is invalid
+        // the whole call is dropped where any offset is invalid (all of these
+        // loads go out together)
+        const int64_t o0 = p.offsets[e], o1 = p.offsets[e + 1];
         bool bad = p.offsets[0] != 0 || p.offsets[p.E] > p.M;
         for (int i = lane; i < p.E; i += 64) bad |= p.offsets[i + 1] < p.offsets[i];
         bad = __ballot(bad) != 0;
         if (t == 0 && threadIdx.x == 0) *p.err = bad ? 1 : 0;
         if (bad) return;
-        const int64_t o0 = p.offsets[e];
-        R = p.offsets[e + 1] - o0;
+        R = o1 - o0;
         const int64_t blk = e + o0 / 128;
         a = p.a + r0 * p.P + 128 * blk;
         lda = p.P;
@@ -189,7 +193,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
             dma_lds_r<16>(ra, (row < rows && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, a));
             dma_lds_r<16>(rb, (row < cols && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, b));
         }
-        const int h = wave & 1, row = 64 * h + lane;
+        const int h = wave & 1, row = s < nb ? 64 * h + lane : 0x7FFFFFFF;
         if (WGRAD && wave >= 2)
             dma_lds_r<4>(rsb, row < cols ? 4u * ((uint32_t)s * (uint32_t)ldbs + (uint32_t)row) : OOB,
                          slot + (uint32_t)offsetof(B128Slot, sb) + 256u * (uint32_t)h);
@@ -204,45 +208,44 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 
-    if (nb > 0) issue(0);
+    // Two stages are in flight: a wave takes all of a stage into registers, and
+    // its slot is refilled with the stage after next before the products begin.
+    issue(0);
+    issue(1);
     for (int s = 0; s < nb; ++s) {
-        if (s + 1 < nb) {
-            issue(s + 1);
-            wait_vmcnt<9>();
-        } else {
-            wait_vmcnt<0>();
-        }
+        wait_vmcnt<9>();
         block_barrier();
         const uint32_t slot = (uint32_t)(s & 1) * (uint32_t)sizeof(B128Slot);
         const float sw = WGRAD ? 1.0f : bs[s * ldbs];
-        int8v fb[4];
+        int8v fa[4], fb[4];
         float4v sb[4];
+        float sc[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t c = (uint32_t)(64 * wn + 16 * j);
+            const uint32_t c = (uint32_t)(64 * wn + 16 * j), r = (uint32_t)(64 * wm + 16 * j);
             fb[j] = b128_frag(lds, slot + (uint32_t)offsetof(B128Slot, b) + 128u * c, lane);
+            fa[j] = b128_frag(lds, slot + (uint32_t)offsetof(B128Slot, a) + 128u * r, lane);
             if constexpr (WGRAD)
                 sb[j] = *(const __attribute__((address_space(3))) float4v*)(
                     lds + slot + (uint32_t)offsetof(B128Slot, sb) + 4u * (c + 4u * (uint32_t)(lane >> 4)));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r = (uint32_t)(64 * wm + 16 * i);
-            const int8v fa = b128_frag(lds, slot + (uint32_t)offsetof(B128Slot, a) + 128u * r, lane);
-            const float sa = *(const __attribute__((address_space(3))) float*)(
+            sc[j] = *(const __attribute__((address_space(3))) float*)(
                 lds + slot + (uint32_t)offsetof(B128Slot, sa) + 4u * (r + (uint32_t)(lane & 15)));
-            const float sc = WGRAD ? sa : sa * sw;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float4v d = b128_mfma(fb[j], fa);
-#pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    acc[i][j][v] = fmaf(WGRAD ? d[v] * sb[j][v] : d[v], sc, acc[i][j][v]);
-            }
         }
         wait_lgkmcnt0();
         block_barrier();
+        issue(s + 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float c = WGRAD ? sc[i] : sc[i] * sw;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4v d = b128_mfma(fb[j], fa[i]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(WGRAD ? d[v] * sb[j][v] : d[v], c, acc[i][j][v]);
+            }
+        }
     }
+    wait_vmcnt<0>();
 
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
     const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
@@ -348,14 +351,15 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         r0 = WT * (4 * g + ll % h);
         c0 = WT * (ll / h);
         rows = (int)min((int64_t)WT, p.R - r0);
-        // the whole call is dropped where any offset is invalid
+        // the whole call is dropped where any offset is invalid (all of these
+        // loads go out together)
+        const int64_t o0 = p.offsets[e], o1 = p.offsets[e + 1];
         bool bad = p.offsets[0] != 0 || p.offsets[p.E] > p.M;
         for (int i = lane; i < p.E; i += 64) bad |= p.offsets[i + 1] < p.offsets[i];
         bad = __ballot(bad) != 0;
         if (t == 0 && threadIdx.x == 0) *p.err = bad ? 1 : 0;
         if (bad) return;
-        const int64_t o0 = p.offsets[e];
-        R = p.offsets[e + 1] - o0;
+        R = o1 - o0;
         const int64_t blk = e + o0 / 128;
         a = p.a + r0 * p.P + 128 * blk;
         lda = p.P;
@@ -650,13 +654,18 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 
 // Which form runs, by the call's sizes:
 //  - at most THIN_ROWS rows an expert on average (not wgrad): 16 x 64 tiles.  32
-//    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles
-//    and 192 of the 128 x 128 ones, 128 rows 165 against 160 and 204.
-//  - 128 x 128 tiles while all of them run at once, two to a compute unit: 3001
-//    rows, 12 experts of 1424 x 2000 30 us against 34 of the 256 x 256 tiles;
-//    one round more, 4096 rows and 1 expert of 4096 x 4096, 92 against 60.
+//    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles;
+//    128 rows 165 against 158.
+//  - 128 x 128 tiles while about all of them run at once, two to a compute unit
+//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 52 us
+//    against 71, 2048 rows 85 to 115 against 88 to 97 with the routing's skew;
+//    and up to TILE_ROWS rows an expert, where most tiles are an expert's last:
+//    32 experts of 4096 x 7168, 1024 rows 197 us against 225, 512 rows 192 against
+//    177, 4096 rows 278 against 287; 64 experts of 2048 x 2048, 4096 rows 52 to 65
+//    against 50 to 69, 16384 rows 115 to 129 against 91 to 124.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
+constexpr int64_t TILE_ROWS = 64;
 constexpr int64_t TILES_AT_ONCE = 512;
 
 template <class K>
@@ -685,9 +694,9 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
     if constexpr (!WGRAD)
         if (a.M <= THIN_ROWS * a.E)
             return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
-    const int64_t ct = (a.C + BT - 1) / BT;
-    const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : max_row_tiles(a.M, a.E, BT) * ct;
-    if (tiles > TILES_AT_ONCE) return launch_wide<F32, WGRAD>(a, s);
+    const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
+    const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
+    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > TILE_ROWS * a.E)) return launch_wide<F32, WGRAD>(a, s);
     // (row tiles in groups of 8)
     return run(k_gemm_b128_tile<F32, WGRAD>, WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct, 256, 0, a, s);
 }

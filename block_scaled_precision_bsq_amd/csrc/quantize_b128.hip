@@ -36,9 +36,11 @@ struct B128Scale {
 __device__ __forceinline__ B128Scale b128_scale(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits << 16);
     const float c = fmaxf(a, B128_TINY);
-    const float y = __builtin_amdgcn_rcpf(c), z = 1.0f / 448.0f;
+    // (c moved towards 1, where its reciprocal is a normal number)
+    const float f = c > 1.0f ? 0x1p-60f : 0x1p60f, d = c * f;
+    const float y = __builtin_amdgcn_rcpf(d), z = 1.0f / 448.0f;
     const float q = 448.0f * y, p = c * z;
-    const float inv = fmaf(fmaf(-c, q, 448.0f), y, q);
+    const float inv = fmaf(fmaf(-d, q, 448.0f), y, q) * f;
     const float scale = fmaf(fmaf(-448.0f, p, c), z, p);
     return {inv, a > 0.0f ? scale : 0.0f};
 }

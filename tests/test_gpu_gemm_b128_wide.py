@@ -1,5 +1,5 @@
 """The 256 x 256 tiles of the FP8B128 grouped GEMMs, which calls of many tiles
-take: the same bounds as test_gpu_gemm_b128.py states, at the edges of a tile
+and rows take: the same bounds as test_gpu_gemm_b128.py states, at the edges of a tile
 (1, 128, 129, 256, 257 rows; partial columns), of the pipeline (one to five
 blocks of 128) and of an expert's rows."""
 import numpy as np
@@ -11,9 +11,9 @@ from test_gpu_gemm_b128 import close, codes, columns, dev, offsets, scales
 
 pytestmark = pytest.mark.gpu
 
-# experts of 0, 1, 128, 129, 256 and 257 rows among small ones
-COUNTS = [1, 0, 128, 129, 256, 257, 3, 17, 0, 64, 100, 31] + [5] * 60 + [0, 2]
-SHAPES = [(1808, 16), (2064, 128), (1808, 144), (2304, 272), (2000, 400), (1856, 640)]  # width, reduction
+# experts of 0, 1, 128, 129, 256, 257 rows and more
+COUNTS = [1, 0, 128, 129, 256, 257, 384, 511]
+SHAPES = [(3984, 16), (4096, 128), (4112, 144), (3984, 272), (4064, 400), (4000, 528)]  # width, reduction
 
 
 @pytest.mark.parametrize("width,red", SHAPES)
@@ -59,7 +59,7 @@ def test_guards_and_invalid_offsets(bsq_gpu):
     """Nothing outside the outputs is written, also where offsets are invalid; repeated calls give the same bits."""
     rng = np.random.default_rng(3)
     off = offsets(COUNTS)
-    E, M, n, k = len(COUNTS), int(off[-1]), 1808, 272
+    E, M, n, k = len(COUNTS), int(off[-1]), 3984, 272
     w, ws = dev(codes(rng, (E * n, k))), dev(scales(rng, (E, -(-n // 128), 3)))
     a, asc = dev(codes(rng, (M, k))), dev(scales(rng, (3, M)))
     buf = torch.full(((M + 4) * n,), 7.0, dtype=torch.bfloat16, device="cuda")

@@ -91,3 +91,22 @@ def test_bad_offsets_stay_in_bounds(bsq_gpu):
         bsq_gpu.bsq_quantize_fp8b128(x, offsets=offd, t=(tc, ts))
         torch.cuda.synchronize()
         assert (buf[:2048] == 7).all() and (buf[2048 + 32 * P:] == 7).all()
+
+
+def test_every_maximum(bsq_gpu):
+    """Each finite bf16 magnitude as a block's maximum, to the type's ends: scales
+    and codes are the correctly rounded quotients' in all three forms."""
+    rng = np.random.default_rng(17)
+    bits = np.arange(1, 0x7F80, dtype=np.uint16)
+    top = torch.from_numpy((bits | (rng.integers(0, 2, bits.size) << 15).astype(np.uint16)).view(np.int16)).view(torch.bfloat16)
+    x = (top.double()[:, None] * torch.from_numpy(rng.uniform(-1, 1, (bits.size, 128)))).bfloat16()
+    x[torch.arange(bits.size), torch.from_numpy(rng.integers(0, 128, bits.size))] = top
+    check(bsq_gpu.bsq_quantize_fp8b128(x.cuda())[0], moe.b128_rows(x.float().numpy()))
+    xt = x.t().contiguous()[:, :32512]  # the same blocks down 128 rows
+    off = np.array([0, 128], np.int32)
+    check(bsq_gpu.bsq_quantize_fp8b128(xt.cuda(), offsets=torch.from_numpy(off).cuda(), rows_form=False)[1],
+          moe.b128_columns(xt.float().numpy(), off))
+    # and over a 128 x 128 block each (of every 64th)
+    w = torch.zeros(128 * 510, 128, dtype=torch.bfloat16)
+    w[::128] = x[::64][:510]
+    check(bsq_gpu.bsq_quantize_fp8b128_weights(w.cuda(), 510), moe.b128_weights(w.float().numpy(), 510))
