@@ -198,3 +198,29 @@ def test_combine_without_rows_or_ye(bsq_gpu):
     off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
     dye, dw = bsq_gpu.bsq_moe_combine_bwd(dy, None, slot, offsets=off, m_total=8, need_dweights=False)
     assert dw is None and (dye[1:3] == 0).all() and (dye[4:] == 0).all()
+
+
+@pytest.mark.parametrize("E,K", [(384, 8), (1024, 20), (256, 6), (130, 5)])
+def test_route_choices_that_share_a_lane(bsq_gpu, E, K):
+    """The first choices at positions 2 l and 2 l + 1 of every 128, in any order, tied
+    among each other, with others before and after them, and zeros of both signs."""
+    rng = np.random.default_rng(E + K)
+    T = 80
+    l = logits_for(rng, T, E, torch.float32, spread=1.0)
+    for t in range(T):
+        lane = int(rng.integers(0, 64))
+        at = np.array([128 * c + 2 * lane + i for c in range(-(-E // 128)) for i in (0, 1)])
+        at = torch.from_numpy(at[at < E])
+        if t % 4 == 0:
+            l[t, at] = 10.0 + torch.from_numpy(rng.permutation(len(at)).astype(np.float32))
+        elif t % 4 == 1:
+            l[t, at] = 10.0                                             # all tied, in one lane
+            l[t, torch.from_numpy(rng.integers(0, E, 3))] = 10.0        # and elsewhere
+        elif t % 4 == 2:
+            l[t] = torch.from_numpy(rng.choice([0.0, -0.0, -1.0], E).astype(np.float32))
+        else:
+            l[t] = torch.from_numpy(np.round(rng.standard_normal(E) * 2).astype(np.float32))
+    bias = np.where(rng.random(E) < 0.5, np.float32(-0.0), np.float32(0.0))
+    check_route(bsq_gpu, l, K, bias=None, normalize=True, seed=1)
+    check_route(bsq_gpu, l, K, bias=bias, normalize=False, seed=2)
+    check_route(bsq_gpu, l.bfloat16(), K, bias=np.round(rng.standard_normal(E)).astype(np.float32), seed=3)
