@@ -109,7 +109,7 @@ struct B128Slot {
     float sb[BT];
 };
 
-template <bool OUT_F32, bool WGRAD>
+template <bool OUT_F32, bool WGRAD, int B_AUX>
 __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     __shared__ __align__(16) B128Slot s_ring[2];
     const int lane = threadIdx.x & 63;
@@ -191,7 +191,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
             const uint32_t ko = 128u * (uint32_t)s + 16u * (uint32_t)((lane & 7) ^ swz8(row));
             const uint32_t dst = slot + 1024u * (uint32_t)(4 * wave + i);
             dma_lds_r<16>(ra, (row < rows && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, a));
-            dma_lds_r<16>(rb, (row < cols && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, b));
+            dma_lds_r<16, B_AUX>(rb, (row < cols && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, b));
         }
         const int h = wave & 1, row = s < nb ? 64 * h + lane : 0x7FFFFFFF;
         if (WGRAD && wave >= 2)
@@ -655,18 +655,26 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 // Which form runs, by the call's sizes:
 //  - at most THIN_ROWS rows an expert on average (not wgrad): 16 x 64 tiles.  32
 //    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles;
-//    128 rows 165 against 158.
+//    128 rows 165 against 158 (148 with the streamed weights below).
 //  - 128 x 128 tiles while about all of them run at once, two to a compute unit
 //    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 52 us
 //    against 71, 2048 rows 85 to 115 against 88 to 97 with the routing's skew;
 //    and up to TILE_ROWS rows an expert, where most tiles are an expert's last:
-//    32 experts of 4096 x 7168, 1024 rows 197 us against 225, 512 rows 192 against
-//    177, 4096 rows 278 against 287; 64 experts of 2048 x 2048, 4096 rows 52 to 65
-//    against 50 to 69, 16384 rows 115 to 129 against 91 to 124.
+//    32 experts of 4096 x 7168, 1024 rows 197 us against 225, 4096 rows 278
+//    against 287; 64 experts of 2048 x 2048, 4096 rows 52 to 65 against 50 to 69,
+//    16384 rows 115 to 129 against 91 to 124.
+//    Their weight loads are non-temporal where hardly a weight is read twice (up
+//    to STREAM_ROWS rows an expert), the weights do not fit the last-level cache
+//    from one call to the next and their rows are whole lines: 32 experts of
+//    4096 x 7168, 128 rows 148 us against 159, 512 rows 180 against 192, but 2048
+//    rows 225 against 211, and 32 experts of 1424 x 2000 (91 MB), 128 rows 27
+//    against 20.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
 constexpr int64_t TILE_ROWS = 64;
+constexpr int64_t STREAM_ROWS = 16;
 constexpr int64_t TILES_AT_ONCE = 512;
+constexpr int64_t LAST_LEVEL_CACHE = (int64_t)256 << 20;
 
 template <class K>
 bsq_status run(K kernel, int64_t grid, int threads, size_t lds, const B128Args& a, hipStream_t s) {
@@ -697,8 +705,11 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
     const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
     const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
     if (tiles > TILES_AT_ONCE && (WGRAD || a.M > TILE_ROWS * a.E)) return launch_wide<F32, WGRAD>(a, s);
-    // (row tiles in groups of 8)
-    return run(k_gemm_b128_tile<F32, WGRAD>, WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct, 256, 0, a, s);
+    if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, tiles, 256, 0, a, s);
+    const int64_t grid = (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
+    const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
+    return stream ? run(k_gemm_b128_tile<F32, false, 2>, grid, 256, 0, a, s)
+                  : run(k_gemm_b128_tile<F32, false, 0>, grid, 256, 0, a, s);
 }
 
 template <bool WGRAD>

@@ -73,3 +73,22 @@ def test_guards_and_invalid_offsets(bsq_gpu):
     assert (buf[:2 * n] == 7).all() and (buf[2 * n + M * n:] == 7).all()
     again = bsq_gpu.bsq_grouped_gemm_fp8b128_fwd((a, asc), (w, ws), dev(off))
     assert torch.equal(again, y)
+
+
+def test_streamed_weights(bsq_gpu):
+    """Few rows against more weights than the caches hold: a row's output is the bits
+    that the same call gives with one expert's weights in place (a product of its own)."""
+    E, n, k, M = 72, 2048, 2048, 300
+    g = torch.Generator(device="cuda").manual_seed(4)
+    w = torch.randint(0, 120, (E * n, k), dtype=torch.uint8, device="cuda", generator=g)
+    ws = torch.rand(E, 16, 16, device="cuda", generator=g)
+    a = torch.randint(0, 120, (M, k), dtype=torch.uint8, device="cuda", generator=g)
+    asc = torch.rand(16, M, device="cuda", generator=g)
+    counts = [4] * 70 + [0, 20]
+    off = offsets(counts)
+    y = bsq_gpu.bsq_grouped_gemm_fp8b128_fwd((a, asc), (w, ws), dev(off))
+    for e in (0, 33, 69, 71):
+        s = slice(int(off[e]), int(off[e + 1]))
+        one = bsq_gpu.bsq_grouped_gemm_fp8b128_fwd((a[s].contiguous(), asc[:, s].contiguous()),
+                                                   (w[e * n:(e + 1) * n], ws[e:e + 1]), dev(offsets([s.stop - s.start])))
+        assert torch.equal(y[s], one)
