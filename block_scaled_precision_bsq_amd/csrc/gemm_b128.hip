@@ -265,8 +265,8 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         }
 }
 
-// 256 x 256 output tiles: 8 waves, two per SIMD, of 128 x 64 (NI = 8 groups of
-// 16 rows; 4 where the tile has at most 128 rows).
+// 256 x CW output tiles: 8 waves, two per SIMD.  CW = 256: waves of 128 x 64 (NI =
+// 8 groups of 16 rows; 4 where the tile has at most 128 rows); CW = 128: of 64 x 64.
 // The stream of operands bounds the loop (its DMA alone takes 69% of the time,
 // its matrix work alone 67%): a compute unit's first-level cache keeps a fixed
 // number of lines in flight and an instruction that finds it full stalls its
@@ -283,36 +283,39 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 // Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 903 us, 2.13
 // PFLOP/s (128 x 128 tiles: 1472 us); dgrad 931 us, wgrad 1400 us.
 constexpr int WT = 256;
+template <int CW>
 struct WideSlot {
     uint8_t a[WT * 128];
-    uint8_t b[WT * 128];  // row 16 j + 4 q + v of each 64 holds output column 16 q + 4 j + v
+    uint8_t b[CW * 128];  // row 16 j + 4 q + v of each 64 holds output column 16 q + 4 j + v
     float sa[WT];
-    float sb[WT];  // wgrad: by output column; else the two 128-column blocks' scales
+    float sb[WT];  // wgrad: by output column; else the 128-column blocks' scales
 };
-constexpr uint32_t WIDE_SLOT = sizeof(WideSlot);
 constexpr int WIDE_X = 12;  // MFMAs before a stage's end at which the slot's reads are over (barrier X)
 constexpr int WIDE_Y = 8;   // and at which the next stage is needed (barrier Y)
-constexpr int WIDE_DMA = 9;  // DMA instructions per wave and stage
-constexpr int WIDE_SPREAD = 18;  // MFMAs over which they go out (half as many in the half-height loop)
+constexpr int wide_dma(int CW) { return 5 + CW / 64; }  // DMA instructions per wave and stage
+constexpr int WIDE_SPREAD = 18;  // MFMAs over which they go out (half as many in the loop of half as many MFMAs)
 
 // DMA instruction n of a stage goes out behind the wide_due(n)th MFMA after X
 // (counted through to the next stage); wide_sent(m): how many go before the mth.
-template <int NI>
-constexpr int wide_due(int n) { return n * (WIDE_SPREAD * NI / 8) / WIDE_DMA; }
-template <int NI>
+template <int CW, int NI>
+constexpr int wide_due(int n) { return n * (WIDE_SPREAD * NI / 8) / wide_dma(CW); }
+template <int CW, int NI>
 constexpr int wide_sent(int m) {
     int c = 0;
-    for (int n = 0; n < WIDE_DMA; ++n) c += wide_due<NI>(n) < m;
+    for (int n = 0; n < wide_dma(CW); ++n) c += wide_due<CW, NI>(n) < m;
     return c;
 }
 
-template <bool OUT_F32, bool WGRAD>
+template <bool OUT_F32, bool WGRAD, int CW>
 __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     extern __shared__ __align__(16) uint8_t s_wide[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wm = wave & 1, wn = wave >> 1;
-    const int CT = (int)((p.C + WT - 1) / WT);
+    constexpr int WM = CW == 256 ? 2 : 4;  // waves down the rows
+    constexpr int WIDE_DMA = wide_dma(CW), BI = CW / 64;
+    constexpr uint32_t WIDE_SLOT = sizeof(WideSlot<CW>);
+    const int wm = wave & (WM - 1), wn = wave / WM;
+    const int CT = (int)((p.C + CW - 1) / CW);
     // 32 consecutive tiles (4 row tiles x 8 column tiles) to an XCD at a time
     const int64_t t = (((int64_t)blockIdx.x >> 8) * 8 + (blockIdx.x & 7)) * 32 + ((blockIdx.x >> 3) & 31);
     int e, rows;
@@ -330,7 +333,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         e = f.e;
         r0 = f.row0;
         rows = (int)min((int64_t)WT, f.end - r0);
-        c0 = WT * (l >> 2);
+        c0 = CW * (l >> 2);
         R = e < p.E ? p.R : 0;
         const int64_t we = e < p.E ? e : 0;
         a = p.a + r0 * p.R;
@@ -349,7 +352,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         const int g = l / (4 * CT), h = min(4, RT - 4 * g);
         const int ll = l - g * 4 * CT;
         r0 = WT * (4 * g + ll % h);
-        c0 = WT * (ll / h);
+        c0 = CW * (ll / h);
         rows = (int)min((int64_t)WT, p.R - r0);
         // the whole call is dropped where any offset is invalid (all of these
         // loads go out together)
@@ -371,7 +374,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         out = static_cast<char*>(p.out) + (((int64_t)e * p.R + r0) * p.C + c0) * (OUT_F32 ? 4 : 2);
     }
     rows = __builtin_amdgcn_readfirstlane(rows);
-    const int cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)WT, p.C - c0));
+    const int cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)CW, p.C - c0));
     const int nb = __builtin_amdgcn_readfirstlane((int)((R + 127) / 128));
     const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)lda);
     const uint32_t lsa = __builtin_amdgcn_readfirstlane((uint32_t)ldas), lsb = __builtin_amdgcn_readfirstlane((uint32_t)ldbs);
@@ -384,13 +387,15 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     const __attribute__((address_space(3))) uint8_t* lds = (const __attribute__((address_space(3))) uint8_t*)(s_wide);
 
     // DMA of stage s into slot s & 1: instructions 2 i and 2 i + 1 move eight
-    // rows of either operand, 8 the scales.
+    // rows of either operand (with 128 columns two more eight of A), the last
+    // one the scales.
     // prep(s) sets the lane offsets of stage s: chunk (lane & 7) ^ swz8(row) of
     // the rows 8 i + lane / 8, even and odd i, or nowhere past the last stage.
     const int drow = lane >> 3;
     const uint32_t ch0 = 16u * (uint32_t)((lane & 7) ^ swz8(drow)), ch1 = 16u * (uint32_t)((lane & 7) ^ swz8(8 + drow));
     const uint32_t abase = (uint32_t)(32 * wave + drow) * ld;
-    const uint32_t bbase = (uint32_t)(64 * (wave >> 1) + 8 * (wave & 1) + 16 * (drow >> 2) + (drow & 3)) * ld;
+    const uint32_t bbase = (uint32_t)((CW == 256 ? 64 * (wave >> 1) + 8 * (wave & 1) : 64 * (wave >> 2) + 4 * (wave & 3)) +
+                                      16 * (drow >> 2) + (drow & 3)) * ld;
     // scales: waves 0..3 those of A, waves 4..7 those of B
     const int srow = 64 * (wave & 3) + lane;
     const bool sb_wave = wave >= 4;
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     const uint32_t scoff = sb_wave ? (WGRAD ? (srow < cols ? 4u * (uint32_t)srow : OOB)
                                             : (srow < (cols + 127) / 128 ? 4u * (uint32_t)(srow * p.bs_c) : OOB))
                                    : (srow < rows ? 4u * (uint32_t)srow : OOB);
-    const uint32_t scdst = (uint32_t)(sb_wave ? offsetof(WideSlot, sb) : offsetof(WideSlot, sa)) + 256u * (uint32_t)(wave & 3);
+    const uint32_t scdst = (uint32_t)(sb_wave ? offsetof(WideSlot<CW>, sb) : offsetof(WideSlot<CW>, sa)) + 256u * (uint32_t)(wave & 3);
     uint32_t va[2], vb[2];
     auto prep = [&](int s) {
         const uint32_t k0 = 128u * (uint32_t)s + ch0, k1 = 128u * (uint32_t)s + ch1;
@@ -410,17 +415,18 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     };
     auto issue = [&](int s, int n) {
         const uint32_t slot = lds0 + (uint32_t)(s & 1) * WIDE_SLOT;
-        const int i = n >> 1;
-        if (n == 8) {
+        if (n == WIDE_DMA - 1) {
             dma_lds_r<4>(rsc, s < nb ? scoff + 4u * (uint32_t)s * lsc : OOB, slot + scdst);
-        } else if (n & 1) {
-            // LDS row 8 i + lane / 8 of the 64: j = i / 2, q = 2 (i & 1) + lane / 32
-            const uint32_t brow = (uint32_t)(4 * (i >> 1) + 32 * (i & 1));
+        } else if ((n & 1) && n < 2 * BI) {
+            // LDS row CW / 8 wave + 8 i + lane / 8
+            const int i = n >> 1;
+            const uint32_t brow = (uint32_t)(CW == 256 ? 4 * (i >> 1) + 32 * (i & 1) : 32 * i);
             dma_lds_r<16>(rb, vb[i & 1] + brow * ld,
-                          slot + 4096u * (uint32_t)wave + (uint32_t)offsetof(WideSlot, b) + 1024u * (uint32_t)i);
+                          slot + (uint32_t)(16 * CW) * (uint32_t)wave + (uint32_t)offsetof(WideSlot<CW>, b) + 1024u * (uint32_t)i);
         } else {
+            const int i = n < 2 * BI ? n >> 1 : n - BI;
             dma_lds_r<16>(ra, va[i & 1] + (uint32_t)(8 * i) * ld,
-                          slot + 4096u * (uint32_t)wave + (uint32_t)offsetof(WideSlot, a) + 1024u * (uint32_t)i);
+                          slot + 4096u * (uint32_t)wave + (uint32_t)offsetof(WideSlot<CW>, a) + 1024u * (uint32_t)i);
         }
     };
 
@@ -436,10 +442,10 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     auto body = [&](auto NIC) {
         constexpr int NI = decltype(NIC)::value;
         constexpr int NM = 4 * NI, XM = NM - WIDE_X, YM = NM - WIDE_Y;
-        const uint32_t fa = (uint32_t)offsetof(WideSlot, a) + (uint32_t)(wm * NI * 16 * 128) + fr, fa1 = fa ^ 64u;
-        const uint32_t fb = (uint32_t)offsetof(WideSlot, b) + (uint32_t)(wn * 64 * 128) + fr, fb1 = fb ^ 64u;
-        const uint32_t fsa = (uint32_t)offsetof(WideSlot, sa) + 4u * (uint32_t)(wm * NI * 16 + lr);
-        const uint32_t fsb = (uint32_t)offsetof(WideSlot, sb) + (WGRAD ? 4u * (uint32_t)(64 * wn + 16 * q) : 4u * (uint32_t)(wn >> 1));
+        const uint32_t fa = (uint32_t)offsetof(WideSlot<CW>, a) + (uint32_t)(wm * NI * 16 * 128) + fr, fa1 = fa ^ 64u;
+        const uint32_t fb = (uint32_t)offsetof(WideSlot<CW>, b) + (uint32_t)(wn * 64 * 128) + fr, fb1 = fb ^ 64u;
+        const uint32_t fsa = (uint32_t)offsetof(WideSlot<CW>, sa) + 4u * (uint32_t)(wm * NI * 16 + lr);
+        const uint32_t fsb = (uint32_t)offsetof(WideSlot<CW>, sb) + (WGRAD ? 4u * (uint32_t)(64 * wn + 16 * q) : 4u * (uint32_t)(64 * wn / 128));
         auto frag = [&](uint32_t at, uint32_t at1) {
             const u32x4 x0 = *(const __attribute__((address_space(3))) u32x4*)(lds + at);
             const u32x4 x1 = *(const __attribute__((address_space(3))) u32x4*)(lds + at1);
@@ -474,8 +480,8 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         };
         // stage 0 and the first instructions of stage 1 are in flight
 #pragma unroll
-        for (int n = 0; n < wide_sent<NI>(NM - XM); ++n) issue(1, n);
-        wait_vmcnt<wide_sent<NI>(NM - XM)>();
+        for (int n = 0; n < wide_sent<CW, NI>(NM - XM); ++n) issue(1, n);
+        wait_vmcnt<wide_sent<CW, NI>(NM - XM)>();
         block_barrier();
 #pragma unroll
         for (int i = 0; i < 3; ++i) rdA(0, i);
@@ -500,7 +506,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
                         block_barrier();
                     }
                     if (m == YM) {
-                        wait_vmcnt<wide_sent<NI>(YM - XM)>();
+                        wait_vmcnt<wide_sent<CW, NI>(YM - XM)>();
                         block_barrier();
                     }
                     const float4v d = b128_mfma(B[j], A[i & 3]);
@@ -521,7 +527,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
                     if (m == XM) prep(s + 2);
 #pragma unroll
                     for (int n = 0; n < WIDE_DMA; ++n)
-                        if (wide_due<NI>(n) == (m >= XM ? m - XM : m - XM + NM)) issue(s + (m >= XM ? 2 : 1), n);
+                        if (wide_due<CW, NI>(n) == (m >= XM ? m - XM : m - XM + NM)) issue(s + (m >= XM ? 2 : 1), n);
                     __builtin_amdgcn_sched_barrier(0);
                 }
                 sc = sc_i;
@@ -549,8 +555,12 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
             }
         }
     };
-    if (rows > 128) body(IC<8>{});
-    else body(IC<4>{});
+    if constexpr (CW == 128) {
+        body(IC<4>{});
+    } else {
+        if (rows > 128) body(IC<8>{});
+        else body(IC<4>{});
+    }
 }
 
 // A row or two an expert: the weights' bytes bound the product, so they go from
@@ -669,11 +679,16 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //    4096 x 7168, 128 rows 148 us against 159, 512 rows 180 against 192, but 2048
 //    rows 225 against 211, and 32 experts of 1424 x 2000 (91 MB), 128 rows 27
 //    against 20.
+//  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
+//    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
+//    x 2000 24 us against 29 and 33; 8 experts of 4096 x 7168, 2048 rows with the
+//    routing's skew would be 94 against 79 and 82, hence the margin.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
 constexpr int64_t TILE_ROWS = 64;
 constexpr int64_t STREAM_ROWS = 16;
 constexpr int64_t TILES_AT_ONCE = 512;
+constexpr int64_t MID_AT_ONCE = 224;
 constexpr int64_t LAST_LEVEL_CACHE = (int64_t)256 << 20;
 
 template <class K>
@@ -683,18 +698,19 @@ bsq_status run(K kernel, int64_t grid, int threads, size_t lds, const B128Args& 
     return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
 }
 
-template <bool F32, bool WGRAD>
+template <bool F32, bool WGRAD, int CW>
 bsq_status launch_wide(const B128Args& a, hipStream_t s) {
-    const int64_t ct = (a.C + WT - 1) / WT;
+    constexpr int lds = 2 * (int)sizeof(WideSlot<CW>);
+    const int64_t ct = (a.C + CW - 1) / CW;
     const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + WT - 1) / WT) * ct : (max_row_tiles(a.M, a.E, WT) + 3) / 4 * 4 * ct;
     static bool attr_set = false;  // idempotent; racing writers set the same value
     if (!attr_set) {
-        if (hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_b128_wide<F32, WGRAD>),
-                                hipFuncAttributeMaxDynamicSharedMemorySize, 2 * WIDE_SLOT) != hipSuccess)
+        if (hipFuncSetAttribute(reinterpret_cast<const void*>(&k_gemm_b128_wide<F32, WGRAD, CW>),
+                                hipFuncAttributeMaxDynamicSharedMemorySize, lds) != hipSuccess)
             return BSQ_ERR_HIP;
         attr_set = true;
     }
-    return run(k_gemm_b128_wide<F32, WGRAD>, (tiles + 255) / 256 * 256, 512, 2 * WIDE_SLOT, a, s);
+    return run(k_gemm_b128_wide<F32, WGRAD, CW>, (tiles + 255) / 256 * 256, 512, lds, a, s);
 }
 
 template <bool F32, bool WGRAD>
@@ -704,7 +720,10 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
             return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
     const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
     const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
-    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > TILE_ROWS * a.E)) return launch_wide<F32, WGRAD>(a, s);
+    if constexpr (!WGRAD)
+        if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= MID_AT_ONCE)
+            return launch_wide<F32, false, 128>(a, s);
+    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > TILE_ROWS * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
     if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, tiles, 256, 0, a, s);
     const int64_t grid = (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
     const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;

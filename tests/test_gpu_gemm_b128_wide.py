@@ -1,4 +1,4 @@
-"""The 256 x 256 tiles of the FP8B128 grouped GEMMs, which calls of many tiles
+"""The 256 x 256 and 256 x 128 tiles of the FP8B128 grouped GEMMs, which calls of many tiles
 and rows take: the same bounds as test_gpu_gemm_b128.py states, at the edges of a tile
 (1, 128, 129, 256, 257 rows; partial columns), of the pipeline (one to five
 blocks of 128) and of an expert's rows."""
@@ -16,12 +16,16 @@ COUNTS = [1, 0, 128, 129, 256, 257, 384, 511]
 SHAPES = [(3984, 16), (4096, 128), (4112, 144), (3984, 272), (4064, 400), (4000, 528)]  # width, reduction
 
 
-@pytest.mark.parametrize("width,red", SHAPES)
-@pytest.mark.parametrize("tail", [0, 300])
-def test_fwd_and_dgrad(bsq_gpu, width, red, tail):
+# fewer rows: 256 x 128 tiles
+MID = [130, 257, 0, 600, 1]
+CASES = [(COUNTS, t, w, r) for w, r in SHAPES for t in (0, 300)] + [(MID, t, w, r) for w, r in SHAPES for t in (0, 9)]
+
+
+@pytest.mark.parametrize("counts,tail,width,red", CASES)
+def test_fwd_and_dgrad(bsq_gpu, counts, tail, width, red):
     rng = np.random.default_rng(width + red)
-    off = offsets(COUNTS)
-    E, M = len(COUNTS), int(off[-1]) + tail
+    off = offsets(counts)
+    E, M = len(counts), int(off[-1]) + tail
     wb, rb = -(-width // 128), -(-red // 128)
     w, ws = codes(rng, (E * width, red)), scales(rng, (E, wb, rb))
     a, asc = codes(rng, (M, red)), scales(rng, (rb, M))
@@ -55,11 +59,12 @@ def test_wgrad(bsq_gpu, n, k, tail):
     assert torch.equal(bsq_gpu.bsq_grouped_gemm_fp8b128_bwd(dev(off), M, n, k, **kw)[1], dw.bfloat16())
 
 
-def test_guards_and_invalid_offsets(bsq_gpu):
+@pytest.mark.parametrize("counts", [COUNTS, MID])
+def test_guards_and_invalid_offsets(bsq_gpu, counts):
     """Nothing outside the outputs is written, also where offsets are invalid; repeated calls give the same bits."""
     rng = np.random.default_rng(3)
-    off = offsets(COUNTS)
-    E, M, n, k = len(COUNTS), int(off[-1]), 3984, 272
+    off = offsets(counts)
+    E, M, n, k = len(counts), int(off[-1]), 3984, 272
     w, ws = dev(codes(rng, (E * n, k))), dev(scales(rng, (E, -(-n // 128), 3)))
     a, asc = dev(codes(rng, (M, k))), dev(scales(rng, (3, M)))
     buf = torch.full(((M + 4) * n,), 7.0, dtype=torch.bfloat16, device="cuda")
