@@ -27,6 +27,7 @@ constexpr int DISPATCH_MAX_BLOCKS = 128;
 // choices per workgroup while there are workgroups to take them (131072 choices:
 // the call 14.4 us; with 2048 or 1024 15.5)
 constexpr int DISPATCH_BLOCK = 4096;
+constexpr int DISPATCH_AHEAD = 4;  // rounds of 64 choices that a wave holds in registers
 
 struct DispatchArgs {
     const int32_t* ids;
@@ -64,28 +65,38 @@ __global__ __launch_bounds__(1024) void k_moe_dispatch_place(DispatchArgs a) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nb = gridDim.x;
     int32_t* mine = s_w[wave];
-    for (int e = lane; e <= a.E; e += 64) mine[e] = 0;
     const int64_t lo = ((int64_t)blockIdx.x * DISPATCH_WAVES + wave) * a.per_wave;
     const int64_t hi = min(a.n, lo + a.per_wave);
-    __syncthreads();
-    for (int64_t i = lo + lane; i < hi; i += 64) atomicAdd(&mine[dispatch_bucket(a, i)], 1);
+    auto bucket = [&](int64_t i) { return i < hi ? dispatch_bucket(a, i) : -1; };
+    // the wave's first choices and (thread e) the workgroups' counts of expert e
+    // are on their way together
+    int ahead[DISPATCH_AHEAD];
+#pragma unroll
+    for (int k = 0; k < DISPATCH_AHEAD; ++k) ahead[k] = bucket(lo + 64 * k + lane);
+    const int e = threadIdx.x;
+    int before = 0, total = 0;
+    if (nb > 1 && e < a.E) {
+#pragma unroll 32
+        for (int b = 0; b < nb; ++b) {
+            const int c = a.counts[(int64_t)b * (a.E + 1) + e];
+            before += b < (int)blockIdx.x ? c : 0;
+            total += c;
+        }
+    }
+    int before_e = 0;  // of bucket E, by lane
+    if (wave == 0)
+        for (int b = lane; b < (int)blockIdx.x; b += 64) before_e += a.counts[(int64_t)b * (a.E + 1) + a.E];
+    for (int i = lane; i <= a.E; i += 64) mine[i] = 0;
+    // (a wave's own counters: its LDS operations are in order)
+#pragma unroll
+    for (int k = 0; k < DISPATCH_AHEAD; ++k)
+        if (ahead[k] >= 0) atomicAdd(&mine[ahead[k]], 1);
+    for (int64_t i = lo + 64 * DISPATCH_AHEAD + lane; i < hi; i += 64) atomicAdd(&mine[dispatch_bucket(a, i)], 1);
     __syncthreads();
     // thread e: the workgroup's counts, those of the workgroups before it and
     // of all, and the waves' counters turned into positions within the expert
-    const int e = threadIdx.x;
-    int before = 0, total = 0;
-    if (e < a.E) {
-        if (nb == 1) {
-            for (int w = 0; w < DISPATCH_WAVES; ++w) total += s_w[w][e];
-        } else {
-#pragma unroll 8
-            for (int b = 0; b < nb; ++b) {
-                const int c = a.counts[(int64_t)b * (a.E + 1) + e];
-                before += b < (int)blockIdx.x ? c : 0;
-                total += c;
-            }
-        }
-    }
+    if (nb == 1 && e < a.E)
+        for (int w = 0; w < DISPATCH_WAVES; ++w) total += s_w[w][e];
     const int incl = wave_scan_i32(total);
     if (lane == 63) s_part[wave] = incl;
     __syncthreads();
@@ -108,8 +119,6 @@ __global__ __launch_bounds__(1024) void k_moe_dispatch_place(DispatchArgs a) {
     }
     if (wave == 0) {
         // bucket E starts after every routed choice
-        int before_e = 0;
-        for (int b = lane; b < (int)blockIdx.x; b += 64) before_e += a.counts[(int64_t)b * (a.E + 1) + a.E];
         int run = routed + __builtin_amdgcn_readlane(wave_scan_i32(before_e), 63);
         if (lane == 0)
             for (int w = 0; w < DISPATCH_WAVES; ++w) {
@@ -120,10 +129,8 @@ __global__ __launch_bounds__(1024) void k_moe_dispatch_place(DispatchArgs a) {
     }
     __syncthreads();
     const int bits = 32 - __builtin_clz(a.E);
-    for (int64_t i0 = lo; i0 < hi; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const bool in = i < hi;
-        const int x = in ? dispatch_bucket(a, i) : 0;
+    auto place = [&](int64_t i, int x) {
+        const bool in = x >= 0;
         uint64_t same = __ballot(in);
         for (int b = 0; b < bits; ++b) {
             const bool bit = (x >> b) & 1;
@@ -137,10 +144,14 @@ __global__ __launch_bounds__(1024) void k_moe_dispatch_place(DispatchArgs a) {
         first = __shfl(first, leader, 64);
         if (in) {
             const int pos = first + __builtin_popcountll(below);
-            a.row_index[pos] = x < a.E ? (int32_t)(i / a.K) : -1;
+            a.row_index[pos] = x < a.E ? (int32_t)((uint32_t)i / (uint32_t)a.K) : -1;
             a.slot[i] = x < a.E ? pos : -1;
         }
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < DISPATCH_AHEAD; ++k)
+        if (lo + 64 * k < hi) place(lo + 64 * k + lane, ahead[k]);
+    for (int64_t i0 = lo + 64 * DISPATCH_AHEAD; i0 < hi; i0 += 64) place(i0 + lane, bucket(i0 + lane));
 }
 
 struct CombineArgs {
