@@ -13,19 +13,19 @@
 
 namespace bsq {
 
-// One step of a row's rotation: op(x, x rotated by N lanes), the two wait
-// states between the write of x and its move included.
-#define BSQ_DPP_STEP(NAME, INSTR, T)                                                                         \
-    template <int N>                                                                                         \
-    __device__ __forceinline__ T NAME(T x) {                                                                 \
-        T r;                                                                                                 \
-        asm("s_nop 1\n\t" INSTR " %0, %1, %1 row_ror:%2 row_mask:0xf bank_mask:0xf" : "=v"(r) : "v"(x), "n"(N)); \
-        return r;                                                                                            \
-    }
-BSQ_DPP_STEP(ror_max_f32, "v_max_f32_dpp", float)
-BSQ_DPP_STEP(ror_add_f32, "v_add_f32_dpp", float)
-BSQ_DPP_STEP(ror_max_i32, "v_max_i32_dpp", int)
-#undef BSQ_DPP_STEP
+// One step of a row's rotation: op(x, x rotated by N lanes).  fmaxf would quiet
+// its operands first, hence the instruction itself, with the two wait states
+// between the write of x and its move.
+template <int N>
+__device__ __forceinline__ float ror_max_f32(float x) {
+    float r;
+    asm("s_nop 1\n\tv_max_f32_dpp %0, %1, %1 row_ror:%2 row_mask:0xf bank_mask:0xf" : "=v"(r) : "v"(x), "n"(N));
+    return r;
+}
+template <int N>
+__device__ __forceinline__ float ror_add_f32(float x) {
+    return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + N, 0xF, 0xF, true));
+}
 
 // x of the lane 16 (32) away within each 32 (64), with the lane's own: {x, y} in
 // either order.
@@ -69,12 +69,17 @@ __device__ __forceinline__ float wave_sum_f32(float x) {
     return __uint_as_float(p.a) + __uint_as_float(p.b);
 }
 
+// (By shifts and row broadcasts to lane 63, whose identity lets the compiler
+// make each step one instruction: 8 instructions less than by rotations.)
 __device__ __forceinline__ int wave_max_i32(int x) {
-    x = ror_max_i32<1>(ror_max_i32<2>(ror_max_i32<4>(ror_max_i32<8>(x))));
-    Pair32 p = swap16((uint32_t)x);
-    x = max((int)p.a, (int)p.b);
-    p = swap32((uint32_t)x);
-    return max((int)p.a, (int)p.b);
+    constexpr int LOWEST = -0x7FFFFFFF - 1;
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x111, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x112, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x114, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x118, 0xF, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x142, 0xA, 0xF, false));
+    x = max(x, __builtin_amdgcn_update_dpp(LOWEST, x, 0x143, 0xC, 0xF, false));
+    return __builtin_amdgcn_readlane(x, 63);
 }
 
 // e^x for x <= 0 from the hardware's 2^y: x log2(e) in two binary32 parts, the

@@ -141,7 +141,7 @@ __device__ __forceinline__ int route_take(RouteBest& b, const int (&key)[VPL], i
     uint64_t who = __ballot(b.k1 == top);
     int l = __builtin_ctzll(who), e = __builtin_amdgcn_readlane(b.p1, l);
     if (who & (who - 1)) {  // a tie across lanes: the lowest position, whose lane it gives
-        e = -__builtin_amdgcn_readfirstlane(wave_max_i32(b.k1 == top ? -b.p1 : KEY_LOST));
+        e = -wave_max_i32(b.k1 == top ? -b.p1 : KEY_LOST);
         l = VPL == 1 ? e : (e & 127) >> 1;
     }
     const bool me = lane == l;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * ROUTE_WAVES) void k_moe_route(RouteArgs a) {
         RouteBest best = route_best<VPL>(key, lane);
         int id = -1;  // lane r < K: the r-th choice
         for (int r = 0; r < a.K; ++r) {
-            const int top = __builtin_amdgcn_readfirstlane(wave_max_i32(best.k1));
+            const int top = wave_max_i32(best.k1);
             if (top <= KEY_NONE) break;
             const int e = route_take<VPL>(best, key, top, lane);
             id = lane == r ? e : id;
