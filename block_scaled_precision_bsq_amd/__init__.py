@@ -525,13 +525,14 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
     if mask is not None:
         _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
     need = bsq_moe_route_workspace_size(T, E)
-    weights, lse, loss = _carve(stream, torch.float32, dev, (T * top_k, T, 1))
+    sizes = T * top_k, E + 1, T * top_k + T + 1
     if workspace is None and need <= _SMALL:
-        ids, counts, ws = _carve(stream, torch.int32, dev, (T * top_k, E + 1), need)
+        ids, counts, floats, ws = _carve(stream, torch.int32, dev, sizes, need)
     else:
-        ids, counts = _carve(stream, torch.int32, dev, (T * top_k, E + 1))
+        ids, counts, floats = _carve(stream, torch.int32, dev, sizes)
         workspace = _scratch(need, workspace, dev, stream)
         ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
+    weights, lse, loss = floats.view(torch.float32).split_with_sizes((T * top_k, T, 1))
     ids, weights = ids.view(T, top_k), weights.view(T, top_k)
     _check("bsq_moe_route",
            _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
@@ -606,13 +607,16 @@ def bsq_moe_combine(ye, slot, weights=None, y=None, stream=None):
     _shaped(slot, "slot", (torch.int32,), (T, K), dev)
     if weights is not None:
         _shaped(weights, "weights", (torch.float32,), (T, K), dev)
+    ldy = W
     if y is None:
         y = _empty(stream, (T, W), dtype=ye.dtype, device=dev)
-    _dev(y, "y", (ye.dtype,))
-    if tuple(y.shape) != (T, W) or y.device != dev:
-        raise ValueError(f"y must have shape {(T, W)} on {dev}")
+    else:
+        _dev(y, "y", (ye.dtype,))
+        if y.shape != (T, W) or y.device != dev:
+            raise ValueError(f"y must have shape {(T, W)} on {dev}")
+        ldy = _rows_ld(y)[2]
     _check("bsq_moe_combine",
-           _lib.bsq_moe_combine(_ptr(ye), dt, M, W, ld, _ptr(slot), _ptr(weights), T, K, _ptr(y), _rows_ld(y)[2],
+           _lib.bsq_moe_combine(_ptr(ye), dt, M, W, ld, _ptr(slot), _ptr(weights), T, K, _ptr(y), ldy,
                                 _stream(stream)))
     return y
 
