@@ -478,6 +478,8 @@ def _dtype_id(t, name):
 
 def _shaped(t, name, dtypes, shape, dev):
     """Checks a dense input or output buffer."""
+    if type(t) is torch.Tensor and t.dtype in dtypes and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t
     _dev(t, name, dtypes)
     if t.shape != shape or not t.is_contiguous() or t.device != dev:
         raise ValueError(f"{name} must be contiguous with shape {tuple(shape)} on {dev}")
@@ -560,12 +562,14 @@ def bsq_moe_route_bwd(logits, expert_ids, weights, lse, counts, dweights=None, d
         _dev(dloss, "dloss", (torch.float32,))
         if dloss.numel() != 1 or dloss.device != dev:
             raise ValueError(f"dloss must hold one value on {dev}")
+    ldd = E
     if dlogits is None:
         dlogits = _empty(stream, (T, E), dtype=logits.dtype, device=dev)
-    _dev(dlogits, "dlogits", (logits.dtype,))
-    if tuple(dlogits.shape) != (T, E) or dlogits.device != dev:
-        raise ValueError(f"dlogits must have shape {(T, E)} on {dev}")
-    ldd = _rows_ld(dlogits)[2]
+    else:
+        _dev(dlogits, "dlogits", (logits.dtype,))
+        if dlogits.shape != (T, E) or dlogits.device != dev:
+            raise ValueError(f"dlogits must have shape {(T, E)} on {dev}")
+        ldd = _rows_ld(dlogits)[2]
     _check("bsq_moe_route_bwd",
            _lib.bsq_moe_route_bwd(_ptr(logits), dt, T, E, max(ld, E), K, _ptr(expert_ids), _ptr(weights), _ptr(lse),
                                   _ptr(counts), _ptr(dweights), _ptr(dloss), int(normalize), scale, loss_coef,
@@ -644,15 +648,18 @@ def bsq_moe_combine_bwd(dy, ye, slot, weights=None, offsets=None, m_total=None, 
             raise ValueError(f"ye must have {W} columns on {dev}")
         ldye = _rows_ld(ye)[2]
     E = 0 if offsets is None else _offsets(offsets, dev)
+    ldd = W
     if dye is None:
         dye = _empty(stream, (M, W), dtype=dy.dtype, device=dev)
-    _dev(dye, "dye", (dy.dtype,))
-    if tuple(dye.shape) != (M, W) or dye.device != dev:
-        raise ValueError(f"dye must have shape {(M, W)} on {dev}")
+    else:
+        _dev(dye, "dye", (dy.dtype,))
+        if dye.shape != (M, W) or dye.device != dev:
+            raise ValueError(f"dye must have shape {(M, W)} on {dev}")
+        ldd = _rows_ld(dye)[2]
     dw = _empty(stream, (T, K), dtype=torch.float32, device=dev) if need_dweights else None
     _check("bsq_moe_combine_bwd",
            _lib.bsq_moe_combine_bwd(_ptr(dy), dt, T, W, ld, _ptr(ye), M, ldye, _ptr(slot), _ptr(weights), K,
-                                    _ptr(offsets), E, _ptr(dye), _rows_ld(dye)[2], _ptr(dw), _stream(stream)))
+                                    _ptr(offsets), E, _ptr(dye), ldd, _ptr(dw), _stream(stream)))
     return dye, dw
 
 
@@ -671,20 +678,23 @@ def bsq_quantize_fp8b128(x, row_index=None, offsets=None, rows_form=True, row=No
         _shaped(row_index, "row_index", (torch.int32,), (rows,), dev)
     nb = (cols + 127) // 128
     G = 0
-    if rows_form:
-        codes, scale = row or (_empty(stream, (rows, cols), dtype=torch.uint8, device=dev),
-                               _empty(stream, (nb, rows), dtype=torch.float32, device=dev))
-        row = (_shaped(codes, "codes", (torch.uint8,), (rows, cols), dev),
-               _shaped(scale, "scale", (torch.float32,), (nb, rows), dev))
-    else:
+    if not rows_form:
         row = None
+    elif row is None:
+        row = (_empty(stream, (rows, cols), dtype=torch.uint8, device=dev),
+               _empty(stream, (nb, rows), dtype=torch.float32, device=dev))
+    else:
+        row = (_shaped(row[0], "codes", (torch.uint8,), (rows, cols), dev),
+               _shaped(row[1], "scale", (torch.float32,), (nb, rows), dev))
     if offsets is not None:
         G = _offsets(offsets, dev)
         Pc = bsq_colwise_padded_cols(G, rows)
-        tc, ts = t or (_empty(stream, (cols, Pc), dtype=torch.uint8, device=dev),
-                       _empty(stream, (Pc // 128, cols), dtype=torch.float32, device=dev))
-        t = (_shaped(tc, "t codes", (torch.uint8,), (cols, Pc), dev),
-             _shaped(ts, "t scale", (torch.float32,), (Pc // 128, cols), dev))
+        if t is None:
+            t = (_empty(stream, (cols, Pc), dtype=torch.uint8, device=dev),
+                 _empty(stream, (Pc // 128, cols), dtype=torch.float32, device=dev))
+        else:
+            t = (_shaped(t[0], "t codes", (torch.uint8,), (cols, Pc), dev),
+                 _shaped(t[1], "t scale", (torch.float32,), (Pc // 128, cols), dev))
     else:
         t = None
     rq, tq = row or (None, None), t or (None, None)
@@ -703,14 +713,13 @@ def bsq_quantize_fp8b128_weights(w, num_experts, transposed=True, codes=None, co
         raise ValueError("w must hold num_experts * n rows")
     n, dev = rows // num_experts, w.device
     sshape = (num_experts, (n + 127) // 128, (k + 127) // 128)
-    codes = _empty(stream, (rows, k), dtype=torch.uint8, device=dev) if codes is None else codes
-    scale = _empty(stream, sshape, dtype=torch.float32, device=dev) if scale is None else scale
-    if transposed and codes_t is None:
-        codes_t = _empty(stream, (num_experts * k, n), dtype=torch.uint8, device=dev)
-    _shaped(codes, "codes", (torch.uint8,), (rows, k), dev)
-    _shaped(scale, "scale", (torch.float32,), sshape, dev)
+    u8, f32 = (torch.uint8,), (torch.float32,)
+    codes = _empty(stream, (rows, k), dtype=u8[0], device=dev) if codes is None else _shaped(codes, "codes", u8, (rows, k), dev)
+    scale = _empty(stream, sshape, dtype=f32[0], device=dev) if scale is None else _shaped(scale, "scale", f32, sshape, dev)
     if codes_t is not None:
-        _shaped(codes_t, "codes_t", (torch.uint8,), (num_experts * k, n), dev)
+        _shaped(codes_t, "codes_t", u8, (num_experts * k, n), dev)
+    elif transposed:
+        codes_t = _empty(stream, (num_experts * k, n), dtype=u8[0], device=dev)
     _check("bsq_quantize_fp8b128_weights",
            _lib.bsq_quantize_fp8b128_weights(_ptr(w), num_experts, n, k, max(ld, k), _ptr(codes), _ptr(codes_t),
                                              _ptr(scale), _stream(stream)))
