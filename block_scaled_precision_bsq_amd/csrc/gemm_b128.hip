@@ -280,8 +280,8 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 // land.  A sum waits two MFMAs for its product, so the vector units work beside
 // the matrix cores: 16 of an MFMA's 32 cycles forward, 32 for wgrad.  B rows go
 // to LDS in an order that leaves a lane 16 adjacent output columns.
-// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 903 us, 2.13
-// PFLOP/s (128 x 128 tiles: 1472 us); dgrad 931 us, wgrad 1400 us.
+// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 886 us, 2.17
+// PFLOP/s (128 x 128 tiles: 1220 us); dgrad 904 us, wgrad 1323 us.
 constexpr int WT = 256;
 template <int CW>
 struct WideSlot {
@@ -538,20 +538,34 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         wait_vmcnt<0>();
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int r = wm * NI * 16 + 16 * i + lr, c = 64 * wn + 16 * q;
-            const uint32_t o = (r < rows && c < cols) ? (uint32_t)r * ldo + (uint32_t)c * (OUT_F32 ? 4u : 2u) : OOB;
+            // Lanes 8 apart swap halves, so that an instruction covers whole lines
+            // of 8 rows instead of every other 16 bytes of 16 rows (wgrad 1385 us
+            // that way), and the stores can be non-temporal (1366 otherwise).
+            const int r = wm * NI * 16 + 16 * i + (lr & 7), c = 64 * wn + 16 * q;
+            const uint32_t up = r < rows && c < cols ? 0u : OOB, dn = r + 8 < rows && c < cols ? 0u : OOB;
+            const uint32_t o = (uint32_t)r * ldo + (uint32_t)c * (OUT_F32 ? 4u : 2u) + (lr & 8 ? 16u : 0u);
+            auto store = [&](const u32x4& x, const u32x4& y, uint32_t at) {  // 32 adjacent bytes
+                u32x4 u, d;
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    u[v] = (uint32_t)__builtin_amdgcn_update_dpp((int)x[v], (int)y[v], 0x128, 0xF, 0xC, false);
+                    d[v] = (uint32_t)__builtin_amdgcn_update_dpp((int)y[v], (int)x[v], 0x128, 0xF, 0x3, false);
+                }
+                __builtin_amdgcn_raw_buffer_store_b128(u, ro, (int)(up | (o + at)), 0, OUT_STORE_NT);
+                __builtin_amdgcn_raw_buffer_store_b128(d, ro, (int)(dn | (o + at + 8u * ldo)), 0, OUT_STORE_NT);
+            };
             if constexpr (OUT_F32) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), ro, (int)(o + 16u * j), 0, 0);
+                for (int h = 0; h < 2; ++h)
+                    store(__builtin_bit_cast(u32x4, acc[i][2 * h]), __builtin_bit_cast(u32x4, acc[i][2 * h + 1]), 32u * h);
             } else {
+                u32x4 x[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    __builtin_amdgcn_raw_buffer_store_b128(
-                        u32x4{pack_bf16x2(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16x2(acc[i][2 * h][2], acc[i][2 * h][3]),
-                              pack_bf16x2(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
-                              pack_bf16x2(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])},
-                        ro, (int)(o + 16u * h), 0, 0);
+                    x[h] = u32x4{pack_bf16x2(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16x2(acc[i][2 * h][2], acc[i][2 * h][3]),
+                                 pack_bf16x2(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
+                                 pack_bf16x2(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
+                store(x[0], x[1], 0u);
             }
         }
     };
