@@ -280,8 +280,10 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 // land.  A sum waits two MFMAs for its product, so the vector units work beside
 // the matrix cores: 16 of an MFMA's 32 cycles forward, 32 for wgrad.  B rows go
 // to LDS in an order that leaves a lane 16 adjacent output columns.
-// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 886 us, 2.17
-// PFLOP/s (128 x 128 tiles: 1220 us); dgrad 904 us, wgrad 1323 us.
+// The last stage's row groups are stored as their sums end, beside its other
+// products (after them: wgrad 1310 us, forward 891).
+// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 896 us, 2.15
+// PFLOP/s (128 x 128 tiles: 1220 us); dgrad 926 us, wgrad 1249 us.
 constexpr int WT = 256;
 template <int CW>
 struct WideSlot {
@@ -436,7 +438,6 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     prep(1);
     const int lr = lane & 15, q = lane >> 4;
     const uint32_t fr = (uint32_t)(128 * lr + 16 * (q ^ swz8(lr)));
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
     const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
 
     auto body = [&](auto NIC) {
@@ -490,54 +491,9 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
         if constexpr (!WGRAD) sw = f32_at(fsb);
         rdS(0, 0);
         rdS(0, 1);
-        for (int s = 0; s < nb; ++s) {
-            // Slot m = 4 i + j: MFMA (i, j), then the sum of the MFMA two
-            // slots back, so that no sum waits for the matrix core.
-#pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const float sc_i = WGRAD ? sa[i & 3] : sa[i & 3] * sw;
-                if constexpr (!WGRAD)
-                    if (i == NI - 1) sw = f32_at((uint32_t)((s + 1) & 1) * WIDE_SLOT + fsb);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int m = 4 * i + j;
-                    if (m == XM) {
-                        wait_lgkmcnt0();
-                        block_barrier();
-                    }
-                    if (m == YM) {
-                        wait_vmcnt<wide_sent<CW, NI>(YM - XM)>();
-                        block_barrier();
-                    }
-                    const float4v d = b128_mfma(B[j], A[i & 3]);
-                    // the sum two slots back
-                    if (j >= 2) add(i, j - 2, sc_i);
-                    else add((i + NI - 1) % NI, j + 2, sc);
-                    D[j] = d;
-                    if (i == 0 && j < 2) rdS(s, j + 2);
-                    if (i == NI - 1 && j >= 2) rdS(s + 1, j - 2);
-                    if (j == 0 && i + 3 < NI) rdA(s, i + 3);
-                    // next stage's first fragments once their registers are free
-                    if (m == YM) rdA(s + 1, 0);
-                    if (m == YM + 2) rdA(s + 1, 1);
-                    if (i == NI - 1) {
-                        if (j == 0) rdA(s + 1, 2);
-                        rdB(s + 1, j);
-                    }
-                    if (m == XM) prep(s + 2);
-#pragma unroll
-                    for (int n = 0; n < WIDE_DMA; ++n)
-                        if (wide_due<CW, NI>(n) == (m >= XM ? m - XM : m - XM + NM)) issue(s + (m >= XM ? 2 : 1), n);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                sc = sc_i;
-            }
-        }
-        add(NI - 1, 2, sc);
-        add(NI - 1, 3, sc);
-        wait_vmcnt<0>();
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
+        // output of row group i, whose sums are complete
+        const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
+        auto store_rows = [&](int i) {
             // Lanes 8 apart swap halves, so that an instruction covers whole lines
             // of 8 rows instead of every other 16 bytes of 16 rows (wgrad 1385 us
             // that way), and the stores can be non-temporal (1366 otherwise).
@@ -546,7 +502,7 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
             const uint32_t o = (uint32_t)r * ldo + (uint32_t)c * (OUT_F32 ? 4u : 2u) + (lr & 8 ? 16u : 0u);
             auto store = [&](const u32x4& x, const u32x4& y, uint32_t at) {  // 32 adjacent bytes
                 u32x4 u, d;
-#pragma unroll
+    #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     u[v] = (uint32_t)__builtin_amdgcn_update_dpp((int)x[v], (int)y[v], 0x128, 0xF, 0xC, false);
                     d[v] = (uint32_t)__builtin_amdgcn_update_dpp((int)y[v], (int)x[v], 0x128, 0xF, 0x3, false);
@@ -555,19 +511,81 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
                 __builtin_amdgcn_raw_buffer_store_b128(d, ro, (int)(dn | (o + at + 8u * ldo)), 0, OUT_STORE_NT);
             };
             if constexpr (OUT_F32) {
-#pragma unroll
+    #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     store(__builtin_bit_cast(u32x4, acc[i][2 * h]), __builtin_bit_cast(u32x4, acc[i][2 * h + 1]), 32u * h);
             } else {
                 u32x4 x[2];
-#pragma unroll
+    #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     x[h] = u32x4{pack_bf16x2(acc[i][2 * h][0], acc[i][2 * h][1]), pack_bf16x2(acc[i][2 * h][2], acc[i][2 * h][3]),
                                  pack_bf16x2(acc[i][2 * h + 1][0], acc[i][2 * h + 1][1]),
                                  pack_bf16x2(acc[i][2 * h + 1][2], acc[i][2 * h + 1][3])};
                 store(x[0], x[1], 0u);
             }
+        };
+        // Slot m = 4 i + j: MFMA (i, j), then the sum of the MFMA two slots back,
+        // so that no sum waits for the matrix core.  The last stage has nothing to
+        // fetch or to read ahead; its row groups leave as they are done.
+        auto stage = [&](int s, auto LASTC) {
+            constexpr bool LAST = decltype(LASTC)::value != 0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const float sc_i = WGRAD ? sa[i & 3] : sa[i & 3] * sw;
+                if constexpr (!WGRAD && !LAST)
+                    if (i == NI - 1) sw = f32_at((uint32_t)((s + 1) & 1) * WIDE_SLOT + fsb);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int m = 4 * i + j;
+                    if (!LAST && m == XM) {
+                        wait_lgkmcnt0();
+                        block_barrier();
+                    }
+                    if constexpr (!LAST)
+                        if (m == YM) {
+                            wait_vmcnt<wide_sent<CW, NI>(YM - XM)>();
+                            block_barrier();
+                        }
+                    const float4v d = b128_mfma(B[j], A[i & 3]);
+                    // the sum two slots back
+                    if (j >= 2) add(i, j - 2, sc_i);
+                    else add((i + NI - 1) % NI, j + 2, sc);
+                    D[j] = d;
+                    if (i == 0 && j < 2) rdS(s, j + 2);
+                    if (j == 0 && i + 3 < NI) rdA(s, i + 3);
+                    if constexpr (LAST) {
+                        if (i > 0 && j == 2) store_rows(i - 1);
+                    } else {
+                        if (i == NI - 1 && j >= 2) rdS(s + 1, j - 2);
+                        // next stage's first fragments once their registers are free
+                        if (m == YM) rdA(s + 1, 0);
+                        if (m == YM + 2) rdA(s + 1, 1);
+                        if (i == NI - 1) {
+                            if (j == 0) rdA(s + 1, 2);
+                            rdB(s + 1, j);
+                        }
+                        if (m == XM) prep(s + 2);
+#pragma unroll
+                        for (int n = 0; n < WIDE_DMA; ++n)
+                            if (wide_due<CW, NI>(n) == (m >= XM ? m - XM : m - XM + NM)) issue(s + (m >= XM ? 2 : 1), n);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                sc = sc_i;
+            }
+        };
+        for (int s = 0; s < nb - 1; ++s) stage(s, IC<0>{});
+        if (nb > 0) {
+            stage(nb - 1, IC<1>{});
+            add(NI - 1, 2, sc);
+            add(NI - 1, 3, sc);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NI - 1; ++i) store_rows(i);
         }
+        store_rows(NI - 1);
+        // nothing is on its way into LDS when the wave ends; the stores may be
+        wait_vmcnt<(OUT_F32 ? 4 : 2) * NI>();
     };
     if constexpr (CW == 128) {
         body(IC<4>{});
