@@ -282,8 +282,9 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
 // to LDS in an order that leaves a lane 16 adjacent output columns.
 // The last stage's row groups are stored as their sums end, beside its other
 // products (after them: wgrad 1310 us, forward 891).
-// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 896 us, 2.15
-// PFLOP/s (128 x 128 tiles: 1220 us); dgrad 926 us, wgrad 1249 us.
+// Measured, 32768 rows x 4096 x 7168 over 32 experts: forward 886 us, 2.17
+// PFLOP/s (128 x 128 tiles: 1220 us); dgrad 920 us, wgrad 1249 us; another card
+// takes 3% longer.
 constexpr int WT = 256;
 template <int CW>
 struct WideSlot {
@@ -699,12 +700,16 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles;
 //    128 rows 165 against 158 (148 with the streamed weights below).
 //  - 128 x 128 tiles while about all of them run at once, two to a compute unit
-//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 52 us
-//    against 71, 2048 rows 85 to 115 against 88 to 97 with the routing's skew;
-//    and up to TILE_ROWS rows an expert, where most tiles are an expert's last:
-//    32 experts of 4096 x 7168, 1024 rows 197 us against 225, 4096 rows 278
-//    against 287; 64 experts of 2048 x 2048, 4096 rows 52 to 65 against 50 to 69,
-//    16384 rows 115 to 129 against 91 to 124.
+//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 50 to
+//    77 us (even experts to the routing's skew) against 68 to 85, 2048 rows 86 to
+//    115 against 99 to 88;
+//    and up to TILE_ROWS rows an expert, where most tiles are an expert's last: 32
+//    experts of 4096 x 7168, 1024 rows 196 us against 222, 2048 rows 213 against
+//    231, 4096 rows 280 against 283.  Half as many where the reduction is shorter
+//    than LONG_R, as the big tiles' stores go out beside products: 32 experts of
+//    7168 x 2048, 1024 rows 95 to 110 us against 95 to 104, 2048 rows 107 to 118
+//    against 99 to 113; 64 experts of 2048 x 2048, 2048 rows 48 to 56 against 45
+//    to 60, 4096 rows 51 to 64 against 47 to 66.
 //    Their weight loads are non-temporal where hardly a weight is read twice (up
 //    to STREAM_ROWS rows an expert), the weights do not fit the last-level cache
 //    from one call to the next and their rows are whole lines: 32 experts of
@@ -713,11 +718,12 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //    against 20.
 //  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
 //    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
-//    x 2000 24 us against 29 and 33; 8 experts of 4096 x 7168, 2048 rows with the
-//    routing's skew would be 94 against 79 and 82, hence the margin.
+//    x 2000 22 us against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
+//    routing's skew would be 93 against 79 and 84, hence the margin.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
 constexpr int64_t TILE_ROWS = 64;
+constexpr int64_t LONG_R = 4096;
 constexpr int64_t STREAM_ROWS = 16;
 constexpr int64_t TILES_AT_ONCE = 512;
 constexpr int64_t MID_AT_ONCE = 224;
@@ -755,7 +761,7 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
     if constexpr (!WGRAD)
         if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= MID_AT_ONCE)
             return launch_wide<F32, false, 128>(a, s);
-    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > TILE_ROWS * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
+    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
     if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, tiles, 256, 0, a, s);
     const int64_t grid = (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
     const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;

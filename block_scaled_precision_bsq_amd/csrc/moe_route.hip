@@ -16,7 +16,7 @@
 // two of its keys: a round of the selection is a wave maximum of the first ones
 // and a pop in the lane that has it; only a lane that gives a third expert
 // looks at its keys again.  The instructions bound the kernel, not its bytes:
-// 16384 x 384 binary32, top 8, take 23 us (25 MB, 5 us at the copy rate), of
+// 16384 x 384 binary32, top 8, take 22 us (25 MB, 5 us at the copy rate), of
 // which about 7 are the launch and the sums at its end; with a scan of all keys in
 // every round 25 us, and 43 us with entries in lane order, position tracking in
 // every round and two workgroups' worth of waves.  More waves do not help
