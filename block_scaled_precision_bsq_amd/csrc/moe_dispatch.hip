@@ -11,7 +11,9 @@
 // Up to DISPATCH_ONE_BLOCK choices run as one workgroup; more run as a
 // counting launch and a placing launch, whose workgroups each add up the
 // counts before them (a few hundred bytes per workgroup and expert, from L2)
-// instead of waiting for a third launch in between.
+// instead of waiting for a third launch in between.  131072 choices of 384
+// experts: 3.0 and 8.1 us, bound by dependent steps (the counts, a scan, one
+// counter per rank), not by their 1.5 MB; 128 choices in 3.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -25,7 +27,7 @@ constexpr int DISPATCH_WAVES = 16;
 constexpr int DISPATCH_ONE_BLOCK = 4096;
 constexpr int DISPATCH_MAX_BLOCKS = 128;
 // choices per workgroup while there are workgroups to take them (131072 choices:
-// the call 14.4 us; with 2048 or 1024 15.5)
+// the call 13.0 us; with 2048 or 1024 15.5)
 constexpr int DISPATCH_BLOCK = 4096;
 constexpr int DISPATCH_AHEAD = 4;  // rounds of 64 choices that a wave holds in registers
 
@@ -200,7 +202,8 @@ __device__ __forceinline__ void st8(void* p, int64_t at, const float (&v)[8]) {
 // y[t] = sum_j w[t][j] ye[slot[t][j]], j ascending, binary32, rounded once.
 // A thread owns 8 columns of one token, so a token's K row pieces are in
 // flight together; a workgroup covers 1024 columns.  Bound by the bytes of the
-// gathered rows.
+// gathered rows: 4096 tokens of 7168 bf16 columns, top 8, 95 us, 5.4 TB/s past
+// L2; 16 tokens 4.3 us.
 template <bool F32>
 __global__ __launch_bounds__(128) void k_moe_combine(CombineArgs a) {
     const int64_t t = blockIdx.x;
@@ -235,6 +238,8 @@ __global__ __launch_bounds__(128) void k_moe_combine(CombineArgs a) {
 // dye[slot[t][j]] = w[t][j] dy[t] and dw[t][j] = <dy[t], ye[slot[t][j]]>: a
 // workgroup per token reads dy[t] once for up to 8 choices.  Rows that no
 // choice owns (past offsets[E]) become zero in the workgroups past the tokens.
+// Bound by its bytes, a read and a write of every routed row: 4096 tokens of 7168
+// bf16 columns, top 8, 177 us, 5.5 TB/s.
 constexpr int COMBINE_TAIL_BLOCKS = 64;
 template <bool F32>
 __global__ __launch_bounds__(256) void k_moe_combine_bwd(CombineArgs a) {
