@@ -20,6 +20,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/bsq.h"
 #include "device_common.h"
 #include "gemm_common.h"
@@ -42,6 +44,7 @@ struct B128Args {
     int64_t bs_e, bs_c, bs_b;  // strides of sB by expert, 128-column block and reduction block
     void* out;
     int32_t* err;    // error word
+    float* part;     // split reductions: [tile of the grid][part][128][128]
 };
 
 // ds_read_b128 fragment of 16 rows x 128 bytes at `base` (rows of 128 bytes,
@@ -109,7 +112,9 @@ struct B128Slot {
     float sb[BT];
 };
 
-template <bool OUT_F32, bool WGRAD, int B_AUX>
+// SPLIT: workgroup (tile, part) sums its share of the tile's blocks and leaves
+// the sums to k_gemm_b128_join.
+template <bool OUT_F32, bool WGRAD, int B_AUX, bool SPLIT = false>
 __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     __shared__ __align__(16) B128Slot s_ring[2];
     const int lane = threadIdx.x & 63;
@@ -172,10 +177,20 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         out = static_cast<char*>(p.out) + (((int64_t)e * p.R + r0) * p.C + c0) * (OUT_F32 ? 4 : 2);
     }
     const int cols = (int)min((int64_t)BT, p.C - c0);
-    const int nb = (int)((R + 127) / 128);
+    int nb = (int)((R + 127) / 128);
     const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)lda);
     // token columns are padded to whole blocks of zeros; k and n are not
-    const uint32_t len = WGRAD ? (uint32_t)nb * 128u : (uint32_t)R;
+    uint32_t len = WGRAD ? (uint32_t)nb * 128u : (uint32_t)R;
+    if constexpr (SPLIT) {
+        const int first = (int)((int64_t)nb * blockIdx.y / gridDim.y), last = (int)((int64_t)nb * (blockIdx.y + 1) / gridDim.y);
+        a += 128 * (int64_t)first;
+        b += 128 * (int64_t)first;
+        as += first * ldas;
+        bs += first * ldbs;
+        nb = last - first;
+        len = min(len - 128u * (uint32_t)first, 128u * (uint32_t)nb);
+        out = reinterpret_cast<char*>(p.part + ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * (BT * BT));
+    }
     const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(a), 0x7FFFFFFFu), rb = rsrc_n(uniform_ptr(b), 0x7FFFFFFFu);
     const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(as), 0x7FFFFFFFu), rsb = rsrc_n(uniform_ptr(bs), 0x7FFFFFFFu);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(&s_ring[0]));
@@ -248,7 +263,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     wait_vmcnt<0>();
 
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
-    const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
+    const uint32_t ldo = (SPLIT ? (uint32_t)BT : (uint32_t)p.C) * (OUT_F32 ? 4u : 2u);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -263,6 +278,56 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
                     u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])}, ro, (int)o,
                     0, 0);
         }
+}
+
+// Adds up the parts of a split reduction, in order: a workgroup takes 32 rows of
+// a tile, a thread 16 columns of one.  A launch of its own rather than the last
+// part's workgroup: no counters to clear before, no fences, an order of its own.
+// Bound by its start and the parts' bytes, which the caches hold: about 5 us.
+template <bool OUT_F32, bool WGRAD>
+__global__ __launch_bounds__(256) void k_gemm_b128_join(B128Args p, int parts) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = blockIdx.x >> 2;
+    const int r = 32 * (blockIdx.x & 3) + (threadIdx.x >> 3), c = 16 * (threadIdx.x & 7);
+    const int CT = (int)((p.C + BT - 1) / BT);
+    int64_t r0, c0;
+    int rows;
+    if constexpr (!WGRAD) {
+        const int64_t g = t / (8 * CT);
+        const int l = (int)(t - g * 8 * CT);
+        const RowTile f = find_row_tile<BT>(p, g * 8 + (l & 7), lane);
+        if (f.e < 0) return;
+        r0 = f.row0;
+        rows = (int)min((int64_t)BT, f.end - r0);
+        c0 = BT * (l >> 3);
+    } else {
+        if (*p.err != 0) return;  // (the launch before this one's)
+        const int RT = (int)((p.R + BT - 1) / BT);
+        const int64_t e = t / (RT * CT);
+        const int l = (int)(t - e * RT * CT);
+        const int first = BT * (l % RT);
+        r0 = e * p.R + first;
+        rows = (int)min((int64_t)BT, p.R - first);
+        c0 = BT * (l / RT);
+    }
+    if (r >= rows || c0 + c >= p.C) return;
+    const float4v* x = reinterpret_cast<const float4v*>(p.part + t * parts * (BT * BT) + BT * r + c);
+    float4v sum[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll 4
+    for (int k = 1; k < parts; ++k)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[v] += x[k * (BT * BT / 4) + v];
+    if constexpr (OUT_F32) {
+        float4v* o = reinterpret_cast<float4v*>(static_cast<float*>(p.out) + (r0 + r) * p.C + c0 + c);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) o[v] = sum[v];
+    } else {
+        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (r0 + r) * p.C + c0 + c);
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+            o[v] = u32x4{pack_bf16x2(sum[2 * v][0], sum[2 * v][1]), pack_bf16x2(sum[2 * v][2], sum[2 * v][3]),
+                         pack_bf16x2(sum[2 * v + 1][0], sum[2 * v + 1][1]), pack_bf16x2(sum[2 * v + 1][2], sum[2 * v + 1][3])};
+    }
 }
 
 // 256 x CW output tiles: 8 waves, two per SIMD.  CW = 256: waves of 128 x 64 (NI =
@@ -699,6 +764,17 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //  - at most THIN_ROWS rows an expert on average (not wgrad): 16 x 64 tiles.  32
 //    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles;
 //    128 rows 165 against 158 (148 with the streamed weights below).
+//  - 128 x 128 tiles in parts along the reduction, as many as run at once
+//    (SPLIT_AT_ONCE) and have room in the workspace, of at least SPLIT_STAGES blocks,
+//    where few tiles have a long one: 8 rows over 2 experts of 304 x 5696 14 us
+//    against 35 in one part, 256 over 4 of 2048 x 7168 30 against 44, 1375 over 13 of
+//    336 x 7104 24 against 43; wgrad of 17618 rows, 2 experts of 272 x 416 25
+//    against 98, 32768 rows, 8 experts of 512 x 512 47 against 99.  From SPLIT_FROM
+//    blocks on (the join takes 5 us and its bytes: 20 blocks 16.6 against 19.0, at
+//    most the same below), SPLIT_LONG where the tiles alone take more than a quarter
+//    of the chip's places (512 rows over 2 experts of 3584 x 4096, 32 blocks, 34
+//    against 29, but 1024 over 4 of 2048 x 7168, 56 blocks, 40 against 45).  wgrad counts twice the experts' average
+//    blocks, as the routing's skew puts most of them on a few.
 //  - 128 x 128 tiles while about all of them run at once, two to a compute unit
 //    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 50 to
 //    77 us (even experts to the routing's skew) against 68 to 85, 2048 rows 86 to
@@ -727,7 +803,15 @@ constexpr int64_t LONG_R = 4096;
 constexpr int64_t STREAM_ROWS = 16;
 constexpr int64_t TILES_AT_ONCE = 512;
 constexpr int64_t MID_AT_ONCE = 224;
+constexpr int64_t SPLIT_AT_ONCE = 512;
+constexpr int64_t SPLIT_STAGES = 6;
+constexpr int64_t SPLIT_FROM = 20;
+constexpr int64_t SPLIT_LONG = 48;
+constexpr int64_t SPLIT_TILES = 512;  // 32 MB of workspace
 constexpr int64_t LAST_LEVEL_CACHE = (int64_t)256 << 20;
+
+// Where the parts of split reductions start in the workspace.
+size_t plan_bytes(int E) { return (size_t)((plan_words(E + 1) * 4 + 255) / 256 * 256); }
 
 template <class K>
 bsq_status run(K kernel, int64_t grid, int threads, size_t lds, const B128Args& a, hipStream_t s) {
@@ -758,12 +842,20 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
             return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
     const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
     const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
+    const int64_t grid = WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
+    const int64_t stages = WGRAD ? (a.M + 127) / 128 * (a.E > 1 ? 2 : 1) / a.E : (a.R + 127) / 128;
+    const int64_t parts = std::min({SPLIT_AT_ONCE / std::max(tiles, (int64_t)1), stages / SPLIT_STAGES, SPLIT_TILES / grid});
+    if (parts > 1 && stages >= (tiles > SPLIT_AT_ONCE / 4 ? SPLIT_LONG : SPLIT_FROM)) {
+        hipLaunchKernelGGL((k_gemm_b128_tile<true, WGRAD, 0, true>), dim3((unsigned)grid, (unsigned)parts), dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return BSQ_ERR_HIP;
+        hipLaunchKernelGGL((k_gemm_b128_join<F32, WGRAD>), dim3((unsigned)(4 * grid)), dim3(256), 0, s, a, (int)parts);
+        return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
+    }
     if constexpr (!WGRAD)
         if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= MID_AT_ONCE)
             return launch_wide<F32, false, 128>(a, s);
     if (tiles > TILES_AT_ONCE && (WGRAD || a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
-    if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, tiles, 256, 0, a, s);
-    const int64_t grid = (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
+    if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, grid, 256, 0, a, s);
     const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
     return stream ? run(k_gemm_b128_tile<F32, false, 2>, grid, 256, 0, a, s)
                   : run(k_gemm_b128_tile<F32, false, 0>, grid, 256, 0, a, s);
@@ -781,7 +873,7 @@ extern "C" {
 
 size_t bsq_grouped_gemm_fp8b128_workspace_size(int32_t num_experts) {
     if (num_experts < 1 || num_experts > bsq::MAX_EXPERTS) return 0;
-    return 2 * (size_t)((bsq::plan_words(num_experts + 1) * 4 + 255) / 256 * 256);
+    return bsq::plan_bytes(num_experts) + (size_t)(bsq::SPLIT_TILES * bsq::BT * bsq::BT * 4);
 }
 
 bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
@@ -803,8 +895,10 @@ bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_s
     if (workspace_bytes < bsq_grouped_gemm_fp8b128_workspace_size(num_experts)) return BSQ_ERR_WORKSPACE_TOO_SMALL;
     if (m_total == 0) return BSQ_OK;
     const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
+    int32_t* err = static_cast<int32_t*>(workspace) + bsq::PLAN_ERR;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     const bsq::B128Args a{a_codes, a_scale, w_codes, w_scale, offsets, num_experts, m_total, k, n, 0,
-                          nb * kb, kb, 1, y, static_cast<int32_t*>(workspace) + bsq::PLAN_ERR};
+                          nb * kb, kb, 1, y, err, part};
     return bsq::launch_b128<false>(a, y_dtype == BSQ_F32, stream);
 }
 
@@ -837,15 +931,16 @@ bsq_status bsq_grouped_gemm_fp8b128_bwd(const uint8_t* dy_codes, const float* dy
     if (workspace_bytes < bsq_grouped_gemm_fp8b128_workspace_size(num_experts)) return BSQ_ERR_WORKSPACE_TOO_SMALL;
     const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
     int32_t* err = static_cast<int32_t*>(workspace) + bsq::PLAN_ERR;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     if (dg && m_total > 0) {
         const bsq::B128Args a{dy_codes, dy_scale, wt_codes, w_scale, offsets, num_experts, m_total, n, k, 0,
-                              nb * kb, 1, kb, dx, err};
+                              nb * kb, 1, kb, dx, err, part};
         const bsq_status st = bsq::launch_b128<false>(a, dx_dtype == BSQ_F32, stream);
         if (st != BSQ_OK) return st;
     }
     if (wg) {
         const bsq::B128Args a{dyt_codes, dyt_scale, xt_codes, xt_scale, offsets, num_experts, m_total, n, k, P,
-                              0, 0, 0, dw, err};
+                              0, 0, 0, dw, err, part};
         return bsq::launch_b128<true>(a, dw_dtype == BSQ_F32, stream);
     }
     return BSQ_OK;

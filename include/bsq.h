@@ -535,8 +535,8 @@ bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts,
  *   dx [m_total][k], dw [E][n][k].
  * offsets: 0 = offsets[0] <= ... <= offsets[E] <= m_total; offsets breaking
  * this make the call do no work (bsq_debug_status on the workspace reports 1).
- * workspace >= bsq_grouped_gemm_fp8b128_workspace_size(num_experts) bytes,
- * 256-byte aligned; scratch.
+ * workspace >= bsq_grouped_gemm_fp8b128_workspace_size(num_experts) bytes (32 MB of
+ * them for partial sums of long reductions), 256-byte aligned; scratch.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP.
  */
 bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
