@@ -778,7 +778,11 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //  - 128 x 128 tiles while about all of them run at once, two to a compute unit
 //    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 50 to
 //    77 us (even experts to the routing's skew) against 68 to 85, 2048 rows 86 to
-//    115 against 99 to 88;
+//    115 against 99 to 88 (7/8 of those places from CROWDED_ROWS rows an expert on,
+//    where the big tiles are fuller and the count is an average: 3083 skewed rows over
+//    28 experts of 1616 x 4160, 494 tiles, 66 us against 51, 3542 over 15 of 1760 x
+//    2336, 483, 46 against 34, but 1536 even rows over 8 of 4096 x 7168, 512, 80
+//    against 90);
 //    and up to TILE_ROWS rows an expert, where most tiles are an expert's last: 32
 //    experts of 4096 x 7168, 1024 rows 196 us against 222, 2048 rows 213 against
 //    231, 4096 rows 280 against 283.  Half as many where the reduction is shorter
@@ -795,14 +799,20 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
 //    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
 //    x 2000 22 us against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
-//    routing's skew would be 93 against 79 and 84, hence the margin.
+//    routing's skew would be 93 against 79 and 84, hence the margin of 1/8; none with
+//    FULL_ROWS rows an expert, where few tiles are an expert's last: 15921 rows of one
+//    expert of 512 x 1952, 250 tiles, 22 against 29 and 33, 8625 of one of 864 x 5168,
+//    234, 47 against 60 and 72, but 4051 over 12 of 1408 x 1184, 231, 25 against 22
+//    and 21.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
 constexpr int64_t TILE_ROWS = 64;
 constexpr int64_t LONG_R = 4096;
 constexpr int64_t STREAM_ROWS = 16;
 constexpr int64_t TILES_AT_ONCE = 512;
-constexpr int64_t MID_AT_ONCE = 224;
+constexpr int64_t CROWDED_ROWS = 96;
+constexpr int64_t MID_AT_ONCE = 256;
+constexpr int64_t FULL_ROWS = 512;
 constexpr int64_t SPLIT_AT_ONCE = 512;
 constexpr int64_t SPLIT_STAGES = 6;
 constexpr int64_t SPLIT_FROM = 20;
@@ -852,9 +862,10 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
         return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
     }
     if constexpr (!WGRAD)
-        if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= MID_AT_ONCE)
+        if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= (a.M < FULL_ROWS * a.E ? MID_AT_ONCE * 7 / 8 : MID_AT_ONCE))
             return launch_wide<F32, false, 128>(a, s);
-    if (tiles > TILES_AT_ONCE && (WGRAD || a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
+    const int64_t at_once = WGRAD || a.M < CROWDED_ROWS * a.E ? TILES_AT_ONCE : TILES_AT_ONCE * 7 / 8;
+    if (tiles > at_once && (WGRAD || a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
     if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, grid, 256, 0, a, s);
     const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
     return stream ? run(k_gemm_b128_tile<F32, false, 2>, grid, 256, 0, a, s)
