@@ -44,7 +44,8 @@ struct B128Args {
     int64_t bs_e, bs_c, bs_b;  // strides of sB by expert, 128-column block and reduction block
     void* out;
     int32_t* err;    // error word
-    float* part;     // split reductions: [tile of the grid][part][128][128]
+    float* part;     // split reductions: [tile][part][128][128]
+    int even;        // 128 x 128 tiles spread evenly over the XCDs
 };
 
 // ds_read_b128 fragment of 16 rows x 128 bytes at `base` (rows of 128 bytes,
@@ -68,35 +69,57 @@ struct RowTile {
     int e;
     int64_t row0, end;
 };
-template <int TM>
-__device__ __forceinline__ RowTile find_row_tile(const B128Args& p, int64_t rt, int lane) {
-    RowTile f{-1, 0, 0};
-    int64_t before = 0;
+// pick(all) names the row tile, from the number of all of them where ALL and p.even.
+template <int TM, bool ALL, class Pick>
+__device__ __forceinline__ RowTile pick_row_tile(const B128Args& p, int lane, Pick pick) {
     bool bad = p.offsets[0] != 0;
-    for (int base = 0; base <= p.E; base += 64) {
+    int64_t lo, hi;
+    int n, incl;
+    auto sizes = [&](int base) {  // of the experts base + lane, their tiles and running count
         const int e = base + lane;
-        int64_t lo = 0, hi = 0;
+        lo = hi = 0;
         if (e <= p.E) {
             lo = p.offsets[e];
             hi = e < p.E ? (int64_t)p.offsets[e + 1] : p.M;
         }
         bad |= __ballot(hi < lo) != 0;
-        const int n = hi > lo ? (int)((hi - lo + TM - 1) / TM) : 0;
-        const int incl = wave_scan_i32(n);
+        n = hi > lo ? (int)((hi - lo + TM - 1) / TM) : 0;
+        incl = wave_scan_i32(n);
+    };
+    sizes(0);
+    int64_t all = __builtin_amdgcn_readlane(incl, 63);
+    if (ALL && p.even && p.E >= 64) {
+        for (int base = 64; base <= p.E; base += 64) {
+            sizes(base);
+            all += __builtin_amdgcn_readlane(incl, 63);
+        }
+        sizes(0);
+    }
+    const int64_t rt = pick(all);
+    RowTile f{-1, 0, 0};
+    int64_t before = 0;
+    for (int base = 0;;) {
         const int64_t at = rt - before;
         const uint64_t in = __ballot(at >= incl - n && at < incl);
         if (in) {
             const int w = __builtin_ctzll(in);
-            f.e = __builtin_amdgcn_readlane(e, w);
+            f.e = base + w;
             const int lo_w = __builtin_amdgcn_readlane((int)lo, w), first = __builtin_amdgcn_readlane(incl - n, w);
             f.end = __builtin_amdgcn_readlane((int)hi, w);
             f.row0 = lo_w + (at - first) * TM;
         }
         before += __builtin_amdgcn_readlane(incl, 63);
+        base += 64;
+        if (base > p.E) break;
+        sizes(base);
     }
     if (bad) f.e = -1;
     if (rt == 0 && lane == 0) *p.err = bad ? 1 : 0;
     return f;
+}
+template <int TM>
+__device__ __forceinline__ RowTile find_row_tile(const B128Args& p, int64_t rt, int lane) {
+    return pick_row_tile<TM, false>(p, lane, [&](int64_t) { return rt; });
 }
 
 // 128 x 128 output tiles: 4 waves of 64 x 64, a ring of two 128-byte stages
@@ -128,17 +151,28 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     int64_t lda, ldas, ldbs;
     char* out;
     int c0;
+    uint32_t tile = blockIdx.x;  // (grids stay below 2^24 workgroups)
     if constexpr (!WGRAD) {
-        // groups of 8 row tiles sweep the column tiles together
-        const int64_t t = blockIdx.x;
-        const int64_t g = t / (8 * CT);
-        const int l = (int)(t - g * 8 * CT);
-        const RowTile f = find_row_tile<BT>(p, g * 8 + (l & 7), lane);
-        if (f.e < 0) return;
+        // An XCD gets every eighth workgroup.  Either eight row tiles sweep the column
+        // tiles together, each on its XCD, or, where all tiles run at once (p.even),
+        // an XCD takes an eighth of them, row by row: as many as the others do.
+        bool on = true;
+        const RowTile f = pick_row_tile<BT, true>(p, lane, [&](int64_t all) {
+            if (p.even) {
+                const uint32_t n = (uint32_t)all * (uint32_t)CT, share = (n + 7) / 8, i = blockIdx.x >> 3;
+                tile = (blockIdx.x & 7) * share + i;
+                on = i < share && tile < n;
+            } else {
+                const uint32_t g = tile / (8u * (uint32_t)CT), l = tile - g * 8u * (uint32_t)CT;
+                tile = (g * 8 + (l & 7)) * (uint32_t)CT + (l >> 3);
+            }
+            return (int64_t)(tile / (uint32_t)CT);
+        });
+        if (f.e < 0 || !on) return;
         e = f.e;
         r0 = f.row0;
         rows = (int)min((int64_t)BT, f.end - r0);
-        c0 = BT * (l >> 3);
+        c0 = BT * (int)(tile % (uint32_t)CT);
         R = e < p.E ? p.R : 0;
         const int64_t we = e < p.E ? e : 0;
         a = p.a + r0 * p.R;
@@ -189,7 +223,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         bs += first * ldbs;
         nb = last - first;
         len = min(len - 128u * (uint32_t)first, 128u * (uint32_t)nb);
-        out = reinterpret_cast<char*>(p.part + ((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * (BT * BT));
+        out = reinterpret_cast<char*>(p.part + (int64_t)(tile * gridDim.y + blockIdx.y) * (BT * BT));
     }
     const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(a), 0x7FFFFFFFu), rb = rsrc_n(uniform_ptr(b), 0x7FFFFFFFu);
     const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(as), 0x7FFFFFFFu), rsb = rsrc_n(uniform_ptr(bs), 0x7FFFFFFFu);
@@ -293,13 +327,11 @@ __global__ __launch_bounds__(256) void k_gemm_b128_join(B128Args p, int parts) {
     int64_t r0, c0;
     int rows;
     if constexpr (!WGRAD) {
-        const int64_t g = t / (8 * CT);
-        const int l = (int)(t - g * 8 * CT);
-        const RowTile f = find_row_tile<BT>(p, g * 8 + (l & 7), lane);
+        const RowTile f = find_row_tile<BT>(p, t / CT, lane);
         if (f.e < 0) return;
         r0 = f.row0;
         rows = (int)min((int64_t)BT, f.end - r0);
-        c0 = BT * (l >> 3);
+        c0 = BT * (t % CT);
     } else {
         if (*p.err != 0) return;  // (the launch before this one's)
         const int RT = (int)((p.R + BT - 1) / BT);
@@ -846,13 +878,14 @@ bsq_status launch_wide(const B128Args& a, hipStream_t s) {
 }
 
 template <bool F32, bool WGRAD>
-bsq_status launch_b128(const B128Args& a, hipStream_t s) {
+bsq_status launch_b128(B128Args a, hipStream_t s) {
     if constexpr (!WGRAD)
         if (a.M <= THIN_ROWS * a.E)
             return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
     const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
     const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
     const int64_t grid = WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
+    a.even = tiles <= TILES_AT_ONCE;
     const int64_t stages = WGRAD ? (a.M + 127) / 128 * (a.E > 1 ? 2 : 1) / a.E : (a.R + 127) / 128;
     const int64_t parts = std::min({SPLIT_AT_ONCE / std::max(tiles, (int64_t)1), stages / SPLIT_STAGES, SPLIT_TILES / grid});
     if (parts > 1 && stages >= (tiles > SPLIT_AT_ONCE / 4 ? SPLIT_LONG : SPLIT_FROM)) {
@@ -909,7 +942,7 @@ bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_s
     int32_t* err = static_cast<int32_t*>(workspace) + bsq::PLAN_ERR;
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     const bsq::B128Args a{a_codes, a_scale, w_codes, w_scale, offsets, num_experts, m_total, k, n, 0,
-                          nb * kb, kb, 1, y, err, part};
+                          nb * kb, kb, 1, y, err, part, 0};
     return bsq::launch_b128<false>(a, y_dtype == BSQ_F32, stream);
 }
 
@@ -945,13 +978,13 @@ bsq_status bsq_grouped_gemm_fp8b128_bwd(const uint8_t* dy_codes, const float* dy
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     if (dg && m_total > 0) {
         const bsq::B128Args a{dy_codes, dy_scale, wt_codes, w_scale, offsets, num_experts, m_total, n, k, 0,
-                              nb * kb, 1, kb, dx, err, part};
+                              nb * kb, 1, kb, dx, err, part, 0};
         const bsq_status st = bsq::launch_b128<false>(a, dx_dtype == BSQ_F32, stream);
         if (st != BSQ_OK) return st;
     }
     if (wg) {
         const bsq::B128Args a{dyt_codes, dyt_scale, xt_codes, xt_scale, offsets, num_experts, m_total, n, k, P,
-                              0, 0, 0, dw, err, part};
+                              0, 0, 0, dw, err, part, 0};
         return bsq::launch_b128<true>(a, dw_dtype == BSQ_F32, stream);
     }
     return BSQ_OK;
