@@ -155,7 +155,9 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     if constexpr (!WGRAD) {
         // An XCD gets every eighth workgroup.  Either eight row tiles sweep the column
         // tiles together, each on its XCD, or, where all tiles run at once (p.even),
-        // an XCD takes an eighth of them, row by row: as many as the others do.
+        // an XCD takes an eighth of them, row by row: as many as the others do (17
+        // row tiles of 11 column tiles 36 us against 55 the other way, where one XCD
+        // gets three of them and another two; many rounds of tiles up to 5% slower).
         bool on = true;
         const RowTile f = pick_row_tile<BT, true>(p, lane, [&](int64_t all) {
             if (p.even) {
@@ -799,22 +801,22 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //  - 128 x 128 tiles in parts along the reduction, as many as run at once
 //    (SPLIT_AT_ONCE) and have room in the workspace, of at least SPLIT_STAGES blocks,
 //    where few tiles have a long one: 8 rows over 2 experts of 304 x 5696 14 us
-//    against 35 in one part, 256 over 4 of 2048 x 7168 30 against 44, 1375 over 13 of
+//    against 35 in one part, 256 over 4 of 2048 x 7168 24 against 44, 1375 over 13 of
 //    336 x 7104 24 against 43; wgrad of 17618 rows, 2 experts of 272 x 416 25
 //    against 98, 32768 rows, 8 experts of 512 x 512 47 against 99.  From SPLIT_FROM
-//    blocks on (the join takes 5 us and its bytes: 20 blocks 16.6 against 19.0, at
+//    blocks on (the join takes 5 us and its bytes: 20 blocks 16.4 against 19.2, at
 //    most the same below), SPLIT_LONG where the tiles alone take more than a quarter
 //    of the chip's places (512 rows over 2 experts of 3584 x 4096, 32 blocks, 34
 //    against 29, but 1024 over 4 of 2048 x 7168, 56 blocks, 40 against 45).  wgrad counts twice the experts' average
 //    blocks, as the routing's skew puts most of them on a few.
 //  - 128 x 128 tiles while about all of them run at once, two to a compute unit
-//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 50 to
-//    77 us (even experts to the routing's skew) against 68 to 85, 2048 rows 86 to
-//    115 against 99 to 88 (7/8 of those places from CROWDED_ROWS rows an expert on,
+//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 49 to
+//    63 us (even experts to the routing's skew) against 68 to 85, 2048 rows 81 to
+//    113 against 99 to 86 (7/8 of those places from CROWDED_ROWS rows an expert on,
 //    where the big tiles are fuller and the count is an average: 3083 skewed rows over
-//    28 experts of 1616 x 4160, 494 tiles, 66 us against 51, 3542 over 15 of 1760 x
-//    2336, 483, 46 against 34, but 1536 even rows over 8 of 4096 x 7168, 512, 80
-//    against 90);
+//    28 experts of 1616 x 4160, 494 tiles, 70 us against 51, 3434 over 17 of 1792 x
+//    976, 483, 26 against 19, but 1536 even rows over 8 of 4096 x 7168, 512, 75
+//    against 90; over random sizes of this kind the big tiles take 9% less);
 //    and up to TILE_ROWS rows an expert, where most tiles are an expert's last: 32
 //    experts of 4096 x 7168, 1024 rows 196 us against 222, 2048 rows 213 against
 //    231, 4096 rows 280 against 283.  Half as many where the reduction is shorter
@@ -831,10 +833,10 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
 //    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
 //    x 2000 22 us against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
-//    routing's skew would be 93 against 79 and 84, hence the margin of 1/8; none with
+//    routing's skew would be 93 against 75 and 83, hence the margin of 1/8; none with
 //    FULL_ROWS rows an expert, where few tiles are an expert's last: 15921 rows of one
-//    expert of 512 x 1952, 250 tiles, 22 against 29 and 33, 8625 of one of 864 x 5168,
-//    234, 47 against 60 and 72, but 4051 over 12 of 1408 x 1184, 231, 25 against 22
+//    expert of 512 x 1952, 250 tiles, 21 against 29 and 33, 19273 over 3 of 304 x 3472,
+//    229, 34 against 40 and 46, but 4051 over 12 of 1408 x 1184, 231, 25 against 20
 //    and 21.
 //  - else 256 x 256 tiles.
 constexpr int64_t THIN_ROWS = 2;
