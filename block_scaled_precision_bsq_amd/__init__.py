@@ -537,7 +537,7 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
     weights, lse, loss = floats.view(torch.float32).split_with_sizes((T * top_k, T, 1))
     ids, weights = ids.view(T, top_k), weights.view(T, top_k)
     _check("bsq_moe_route",
-           _lib.bsq_moe_route(_ptr(logits), dt, T, E, max(ld, E), top_k, _ptr(bias), _ptr(mask), int(normalize),
+           _lib.bsq_moe_route(_ptr(logits), dt, T, E, ld, top_k, _ptr(bias), _ptr(mask), int(normalize),
                               scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss), ws, need,
                               _stream(stream)))
     return ids, weights, lse, counts, loss
@@ -571,9 +571,9 @@ def bsq_moe_route_bwd(logits, expert_ids, weights, lse, counts, dweights=None, d
             raise ValueError(f"dlogits must have shape {(T, E)} on {dev}")
         ldd = _rows_ld(dlogits)[2]
     _check("bsq_moe_route_bwd",
-           _lib.bsq_moe_route_bwd(_ptr(logits), dt, T, E, max(ld, E), K, _ptr(expert_ids), _ptr(weights), _ptr(lse),
+           _lib.bsq_moe_route_bwd(_ptr(logits), dt, T, E, ld, K, _ptr(expert_ids), _ptr(weights), _ptr(lse),
                                   _ptr(counts), _ptr(dweights), _ptr(dloss), int(normalize), scale, loss_coef,
-                                  _ptr(dlogits), max(ldd, E), _stream(stream)))
+                                  _ptr(dlogits), ldd, _stream(stream)))
     return dlogits
 
 
@@ -699,7 +699,7 @@ def bsq_quantize_fp8b128(x, row_index=None, offsets=None, rows_form=True, row=No
         t = None
     rq, tq = row or (None, None), t or (None, None)
     _check("bsq_quantize_fp8b128",
-           _lib.bsq_quantize_fp8b128(_ptr(x), src_rows, cols, max(ld, cols), _ptr(row_index), rows, _ptr(offsets), G,
+           _lib.bsq_quantize_fp8b128(_ptr(x), src_rows, cols, ld, _ptr(row_index), rows, _ptr(offsets), G,
                                      _ptr(rq[0]), _ptr(rq[1]), _ptr(tq[0]), _ptr(tq[1]), _stream(stream)))
     return row, t
 
@@ -721,7 +721,7 @@ def bsq_quantize_fp8b128_weights(w, num_experts, transposed=True, codes=None, co
     elif transposed:
         codes_t = _empty(stream, (num_experts * k, n), dtype=u8[0], device=dev)
     _check("bsq_quantize_fp8b128_weights",
-           _lib.bsq_quantize_fp8b128_weights(_ptr(w), num_experts, n, k, max(ld, k), _ptr(codes), _ptr(codes_t),
+           _lib.bsq_quantize_fp8b128_weights(_ptr(w), num_experts, n, k, ld, _ptr(codes), _ptr(codes_t),
                                              _ptr(scale), _stream(stream)))
     return codes, codes_t, scale
 
