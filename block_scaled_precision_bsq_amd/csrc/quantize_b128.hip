@@ -355,10 +355,11 @@ bsq_status bsq_quantize_fp8b128(const void* x_bf16, int64_t src_rows, int64_t co
     if (src_rows < 0 || cols < 0 || rows < 0 || num_groups < 0) return BSQ_ERR_INVALID_ARG;
     if ((codes == nullptr) != (scale == nullptr) || (t_codes == nullptr) != (t_scale == nullptr))
         return BSQ_ERR_INVALID_ARG;
-    if (!codes && !t_codes) return BSQ_ERR_INVALID_ARG;
-    if (!row_index && rows != src_rows) return BSQ_ERR_INVALID_ARG;
+    if (cols == 0) return BSQ_OK;
+    // (without rows the row form has no bytes, and an index no address)
+    if (rows > 0 && ((!codes && !t_codes) || (!row_index && rows != src_rows))) return BSQ_ERR_INVALID_ARG;
     if (t_codes && (!offsets || num_groups < 1)) return BSQ_ERR_INVALID_ARG;
-    if (cols == 0 || (rows == 0 && !t_codes)) return BSQ_OK;
+    if (rows == 0 && !t_codes) return BSQ_OK;
     if ((src_rows > 0 && rows > 0 && !x_bf16) || ld_x < cols) return BSQ_ERR_INVALID_ARG;
     if (cols % 16 || ld_x % 8 || !bsq::al(x_bf16, 16) || !bsq::al(codes, 16) || !bsq::al(t_codes, 16) ||
         !bsq::al(scale, 4) || !bsq::al(t_scale, 4) || !bsq::al(row_index, 4) || !bsq::al(offsets, 4))

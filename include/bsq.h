@@ -500,8 +500,8 @@ bsq_status bsq_moe_combine_bwd(const void* dy, bsq_dtype dtype, int64_t tokens, 
  *     [E][ceil(n/128)][ceil(k/128)] (one array for both orientations).
  *
  * bsq_quantize_fp8b128 -- row and / or token-column form of x[row_index] (x
- * itself when row_index is NULL, then rows == src_rows); an index outside
- * [0, src_rows) gives a zero row.  codes/scale or t_codes/t_scale may be NULL
+ * itself when row_index is NULL, then rows == src_rows, or rows == 0); an index
+ * outside [0, src_rows) gives a zero row.  codes/scale or t_codes/t_scale may be NULL
  * (not wanted).  offsets/num_groups (device, as for BSQ_COLWISE_T) are needed
  * for the token columns; rows past offsets[num_groups] are in no column.  With
  * both forms one read serves both, and offsets[0] must be 0.
