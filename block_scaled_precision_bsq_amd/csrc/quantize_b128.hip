@@ -5,7 +5,9 @@
 //
 // A block with maximum magnitude a: c = max(a, 2^-100), code of x =
 // E4M3_RNE(RN(x * RN(448 / c))) (saturating: the product may round past 448),
-// scale = RN(c / 448), and 0 for an all-zero block.  The two divisions are
+// scale = RN(c / 448), and 0 for an all-zero block; a block that holds an
+// infinity or a NaN gets a NaN scale (as magnitude bits those order above all
+// finite numbers), so no element of it passes for a number.  The two divisions are
 // correctly rounded, once per block; an element costs an unpack, a multiply and
 // its share of a packed conversion.  The product is below 448 (1 + 2^-23), which
 // rounds to 448, so there is no clamp.  With few enough instructions around
@@ -36,14 +38,15 @@ struct B128Scale {
 // from the middle of two.
 __device__ __forceinline__ B128Scale b128_scale(uint32_t amax_bits) {
     const float a = __uint_as_float(amax_bits << 16);
-    const float c = fmaxf(a, B128_TINY);
+    // (no maximum: a NaN has to stay; an infinite c gives 0 * inf below)
+    const float c = a < B128_TINY ? B128_TINY : a;
     // (c moved towards 1, where its reciprocal is a normal number)
     const float f = c > 1.0f ? 0x1p-60f : 0x1p60f, d = c * f;
     const float y = __builtin_amdgcn_rcpf(d), z = 1.0f / 448.0f;
     const float q = 448.0f * y, p = c * z;
     const float inv = fmaf(fmaf(-d, q, 448.0f), y, q) * f;
     const float scale = fmaf(fmaf(-448.0f, p, c), z, p);
-    return {inv, a > 0.0f ? scale : 0.0f};
+    return {inv, a == 0.0f ? 0.0f : scale};
 }
 
 // E4M3 bytes of four floats of magnitude below 464, a in the lowest byte.

@@ -489,7 +489,8 @@ bsq_status bsq_moe_combine_bwd(const void* dy, bsq_dtype dtype, int64_t tokens, 
 /*
  * FP8B128: E4M3 codes with one fp32 scale per 128 elements.  A block with
  * maximum magnitude a: c = max(a, 2^-100), code = E4M3_RNE_sat(RN32(x *
- * RN32(448 / c))), scale = RN32(c / 448), or 0 when a == 0.
+ * RN32(448 / c))), scale = RN32(c / 448), or 0 when a == 0.  A block that holds an
+ * infinity or a NaN gets a NaN scale and unspecified codes: every value of it is NaN.
  *   rows (activations): 1 x 128 along the row; codes [rows][cols], scale
  *     block-major [ceil(cols/128)][rows].
  *   token columns (weight-gradient operands): 128 x 1 down the rows of each
