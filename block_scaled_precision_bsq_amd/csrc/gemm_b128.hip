@@ -17,6 +17,10 @@
 // each 16 x 16 tile: one row scale per lane, and stores of adjacent columns.
 // Any order of t inside a block gives the same sum as long as both operands
 // use it: lane l takes 16-byte chunks l / 16 and 4 + l / 16 of a 128-byte row.
+//
+// Every tile size adds the blocks one after the other, by the same operations: what
+// a row gets (wgrad: an expert) is the same bits whatever else the call holds.  No
+// reduction is split, so few tiles with a long one get smaller tiles instead.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -44,8 +48,7 @@ struct B128Args {
     int64_t bs_e, bs_c, bs_b;  // strides of sB by expert, 128-column block and reduction block
     void* out;
     int32_t* err;    // error word
-    float* part;     // split reductions: [tile][part][128][128]
-    int even;        // 128 x 128 tiles spread evenly over the XCDs
+    int even;        // tiles spread evenly over the XCDs (k_gemm_b128_tile)
 };
 
 // ds_read_b128 fragment of 16 rows x 128 bytes at `base` (rows of 128 bytes,
@@ -122,24 +125,27 @@ __device__ __forceinline__ RowTile find_row_tile(const B128Args& p, int64_t rt, 
     return pick_row_tile<TM, false>(p, lane, [&](int64_t) { return rt; });
 }
 
-// 128 x 128 output tiles: 4 waves of 64 x 64, a ring of two 128-byte stages
-// per operand filled by buffer-to-LDS DMA, two workgroups per CU.  A stage's
-// products take a fraction of its loads' latency, so two stages are in flight:
-// 3001 rows over 12 experts of 1424 x 2000 28.9 us (with one 30.3; 12 us are the
-// host's), 1024 rows over 32 experts of 4096 x 7168 197 us (273).
-constexpr int BT = 128;
+// BT x BT output tiles, BT 32, 64 or 128: 4 waves of BT/2 x BT/2, a ring of two
+// 128-byte stages per operand filled by buffer-to-LDS DMA, two workgroups or more per
+// CU.  A stage's products take a fraction of its loads' latency, so two stages are in
+// flight: 3001 rows over 12 experts of 1424 x 2000 28.9 us with BT 128 (with one 30.3;
+// 12 us are the host's), 1024 rows over 32 experts of 4096 x 7168 197 us (273); three or
+// four of them with BT 64 change nothing.  Where rows are few the weights' bytes bound
+// it: 64 rows over 32 experts of 4096 x 7168 120 us with BT 64, 6.4 TB/s.
+template <int BT>
 struct B128Slot {
     uint8_t a[BT * 128];
     uint8_t b[BT * 128];
-    float sa[BT];
-    float sb[BT];
+    float sa[BT < 64 ? 64 : BT];  // (a DMA instruction writes 64 lanes' words)
+    float sb[BT < 64 ? 64 : BT];
 };
 
-// SPLIT: workgroup (tile, part) sums its share of the tile's blocks and leaves
-// the sums to k_gemm_b128_join.
-template <bool OUT_F32, bool WGRAD, int B_AUX, bool SPLIT = false>
+template <bool OUT_F32, bool WGRAD, int BT, int B_AUX>
 __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
-    __shared__ __align__(16) B128Slot s_ring[2];
+    constexpr int NG = BT / 32;        // groups of 16 rows, and of 16 columns, of a wave
+    constexpr int DMAS = 2 * NG + 1;   // DMA instructions per wave and stage
+    typedef B128Slot<BT> Slot;
+    __shared__ __align__(16) Slot s_ring[2];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave & 1, wn = wave >> 1;
@@ -154,10 +160,11 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     uint32_t tile = blockIdx.x;  // (grids stay below 2^24 workgroups)
     if constexpr (!WGRAD) {
         // An XCD gets every eighth workgroup.  Either eight row tiles sweep the column
-        // tiles together, each on its XCD, or, where all tiles run at once (p.even),
-        // an XCD takes an eighth of them, row by row: as many as the others do (17
-        // row tiles of 11 column tiles 36 us against 55 the other way, where one XCD
-        // gets three of them and another two; many rounds of tiles up to 5% slower).
+        // tiles together, each on its XCD, or (p.even: where all tiles run at once, and
+        // the smaller tiles) an XCD takes an eighth of them, row by row: as many as the
+        // others do (17 row tiles of 11 column tiles 36 us against 55 the other way,
+        // where one XCD gets three of them and another two; many rounds of 128 x 128
+        // tiles up to 5% slower).
         bool on = true;
         const RowTile f = pick_row_tile<BT, true>(p, lane, [&](int64_t all) {
             if (p.even) {
@@ -182,7 +189,7 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         as = p.as + r0;
         ldas = p.M;
         b = p.b + (we * p.C + c0) * p.R;
-        bs = p.bs + we * p.bs_e + (int64_t)(c0 / BT) * p.bs_c;
+        bs = p.bs + we * p.bs_e + (int64_t)(c0 / 128) * p.bs_c;
         ldbs = p.bs_b;
         out = static_cast<char*>(p.out) + (r0 * p.C + c0) * (OUT_F32 ? 4 : 2);
     } else {
@@ -213,83 +220,74 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
         out = static_cast<char*>(p.out) + (((int64_t)e * p.R + r0) * p.C + c0) * (OUT_F32 ? 4 : 2);
     }
     const int cols = (int)min((int64_t)BT, p.C - c0);
-    int nb = (int)((R + 127) / 128);
+    const int nb = (int)((R + 127) / 128);
     const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)lda);
     // token columns are padded to whole blocks of zeros; k and n are not
-    uint32_t len = WGRAD ? (uint32_t)nb * 128u : (uint32_t)R;
-    if constexpr (SPLIT) {
-        const int first = (int)((int64_t)nb * blockIdx.y / gridDim.y), last = (int)((int64_t)nb * (blockIdx.y + 1) / gridDim.y);
-        a += 128 * (int64_t)first;
-        b += 128 * (int64_t)first;
-        as += first * ldas;
-        bs += first * ldbs;
-        nb = last - first;
-        len = min(len - 128u * (uint32_t)first, 128u * (uint32_t)nb);
-        out = reinterpret_cast<char*>(p.part + (int64_t)(tile * gridDim.y + blockIdx.y) * (BT * BT));
-    }
+    const uint32_t len = WGRAD ? (uint32_t)nb * 128u : (uint32_t)R;
     const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(a), 0x7FFFFFFFu), rb = rsrc_n(uniform_ptr(b), 0x7FFFFFFFu);
     const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(as), 0x7FFFFFFFu), rsb = rsrc_n(uniform_ptr(bs), 0x7FFFFFFFu);
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_addr(&s_ring[0]));
     const __attribute__((address_space(3))) uint8_t* lds =
         (const __attribute__((address_space(3))) uint8_t*)(&s_ring[0]);
 
-    // Stage s into slot s & 1; 9 DMA instructions per wave.
+    // Stage s into slot s & 1.
     auto issue = [&](int s) {
-        const uint32_t slot = lds0 + (uint32_t)(s & 1) * (uint32_t)sizeof(B128Slot);
+        const uint32_t slot = lds0 + (uint32_t)(s & 1) * (uint32_t)sizeof(Slot);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 32 * wave + 8 * i + (lane >> 3);
+        for (int i = 0; i < NG; ++i) {
+            const int row = 8 * (NG * wave + i) + (lane >> 3);
             const uint32_t ko = 128u * (uint32_t)s + 16u * (uint32_t)((lane & 7) ^ swz8(row));
-            const uint32_t dst = slot + 1024u * (uint32_t)(4 * wave + i);
-            dma_lds_r<16>(ra, (row < rows && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, a));
-            dma_lds_r<16, B_AUX>(rb, (row < cols && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(B128Slot, b));
+            const uint32_t dst = slot + 1024u * (uint32_t)(NG * wave + i);
+            dma_lds_r<16>(ra, (row < rows && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(Slot, a));
+            dma_lds_r<16, B_AUX>(rb, (row < cols && ko < len) ? (uint32_t)row * ld + ko : OOB, dst + (uint32_t)offsetof(Slot, b));
         }
-        const int h = wave & 1, row = s < nb ? 64 * h + lane : 0x7FFFFFFF;
+        // (the same words twice where there are more waves than halves)
+        const int h = BT == 128 ? wave & 1 : 0, row = s < nb ? 64 * h + lane : 0x7FFFFFFF;
         if (WGRAD && wave >= 2)
             dma_lds_r<4>(rsb, row < cols ? 4u * ((uint32_t)s * (uint32_t)ldbs + (uint32_t)row) : OOB,
-                         slot + (uint32_t)offsetof(B128Slot, sb) + 256u * (uint32_t)h);
+                         slot + (uint32_t)offsetof(Slot, sb) + 256u * (uint32_t)h);
         else
             dma_lds_r<4>(rsa, row < rows ? 4u * ((uint32_t)s * (uint32_t)ldas + (uint32_t)row) : OOB,
-                         slot + (uint32_t)offsetof(B128Slot, sa) + 256u * (uint32_t)h);
+                         slot + (uint32_t)offsetof(Slot, sa) + 256u * (uint32_t)h);
     };
 
-    float4v acc[4][4];
+    float4v acc[NG][NG];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < NG; ++j) acc[i][j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
 
     // Two stages are in flight: a wave takes all of a stage into registers, and
     // its slot is refilled with the stage after next before the products begin.
     issue(0);
     issue(1);
     for (int s = 0; s < nb; ++s) {
-        wait_vmcnt<9>();
+        wait_vmcnt<DMAS>();
         block_barrier();
-        const uint32_t slot = (uint32_t)(s & 1) * (uint32_t)sizeof(B128Slot);
+        const uint32_t slot = (uint32_t)(s & 1) * (uint32_t)sizeof(Slot);
         const float sw = WGRAD ? 1.0f : bs[s * ldbs];
-        int8v fa[4], fb[4];
-        float4v sb[4];
-        float sc[4];
+        int8v fa[NG], fb[NG];
+        float4v sb[NG];
+        float sc[NG];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t c = (uint32_t)(64 * wn + 16 * j), r = (uint32_t)(64 * wm + 16 * j);
-            fb[j] = b128_frag(lds, slot + (uint32_t)offsetof(B128Slot, b) + 128u * c, lane);
-            fa[j] = b128_frag(lds, slot + (uint32_t)offsetof(B128Slot, a) + 128u * r, lane);
+        for (int j = 0; j < NG; ++j) {
+            const uint32_t c = (uint32_t)(16 * (NG * wn + j)), r = (uint32_t)(16 * (NG * wm + j));
+            fb[j] = b128_frag(lds, slot + (uint32_t)offsetof(Slot, b) + 128u * c, lane);
+            fa[j] = b128_frag(lds, slot + (uint32_t)offsetof(Slot, a) + 128u * r, lane);
             if constexpr (WGRAD)
                 sb[j] = *(const __attribute__((address_space(3))) float4v*)(
-                    lds + slot + (uint32_t)offsetof(B128Slot, sb) + 4u * (c + 4u * (uint32_t)(lane >> 4)));
+                    lds + slot + (uint32_t)offsetof(Slot, sb) + 4u * (c + 4u * (uint32_t)(lane >> 4)));
             sc[j] = *(const __attribute__((address_space(3))) float*)(
-                lds + slot + (uint32_t)offsetof(B128Slot, sa) + 4u * (r + (uint32_t)(lane & 15)));
+                lds + slot + (uint32_t)offsetof(Slot, sa) + 4u * (r + (uint32_t)(lane & 15)));
         }
         wait_lgkmcnt0();
         block_barrier();
         issue(s + 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < NG; ++i) {
             const float c = WGRAD ? sc[i] : sc[i] * sw;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < NG; ++j) {
                 const float4v d = b128_mfma(fb[j], fa[i]);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(WGRAD ? d[v] * sb[j][v] : d[v], c, acc[i][j][v]);
@@ -299,12 +297,12 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     wait_vmcnt<0>();
 
     const __amdgpu_buffer_rsrc_t ro = make_rsrc(uniform_ptr(out), 0x7FFFFFFFu);
-    const uint32_t ldo = (SPLIT ? (uint32_t)BT : (uint32_t)p.C) * (OUT_F32 ? 4u : 2u);
+    const uint32_t ldo = (uint32_t)p.C * (OUT_F32 ? 4u : 2u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NG; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int r = 64 * wm + 16 * i + (lane & 15), c = 64 * wn + 16 * j + 4 * (lane >> 4);
+        for (int j = 0; j < NG; ++j) {
+            const int r = 16 * (NG * wm + i) + (lane & 15), c = 16 * (NG * wn + j) + 4 * (lane >> 4);
             const bool ok = r < rows && c < cols;
             const uint32_t o = ok ? (uint32_t)r * ldo + (uint32_t)c * (OUT_F32 ? 4u : 2u) : OOB;
             if constexpr (OUT_F32)
@@ -314,54 +312,6 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
                     u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])}, ro, (int)o,
                     0, 0);
         }
-}
-
-// Adds up the parts of a split reduction, in order: a workgroup takes 32 rows of
-// a tile, a thread 16 columns of one.  A launch of its own rather than the last
-// part's workgroup: no counters to clear before, no fences, an order of its own.
-// Bound by its start and the parts' bytes, which the caches hold: about 5 us.
-template <bool OUT_F32, bool WGRAD>
-__global__ __launch_bounds__(256) void k_gemm_b128_join(B128Args p, int parts) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = blockIdx.x >> 2;
-    const int r = 32 * (blockIdx.x & 3) + (threadIdx.x >> 3), c = 16 * (threadIdx.x & 7);
-    const int CT = (int)((p.C + BT - 1) / BT);
-    int64_t r0, c0;
-    int rows;
-    if constexpr (!WGRAD) {
-        const RowTile f = find_row_tile<BT>(p, t / CT, lane);
-        if (f.e < 0) return;
-        r0 = f.row0;
-        rows = (int)min((int64_t)BT, f.end - r0);
-        c0 = BT * (t % CT);
-    } else {
-        if (*p.err != 0) return;  // (the launch before this one's)
-        const int RT = (int)((p.R + BT - 1) / BT);
-        const int64_t e = t / (RT * CT);
-        const int l = (int)(t - e * RT * CT);
-        const int first = BT * (l % RT);
-        r0 = e * p.R + first;
-        rows = (int)min((int64_t)BT, p.R - first);
-        c0 = BT * (l / RT);
-    }
-    if (r >= rows || c0 + c >= p.C) return;
-    const float4v* x = reinterpret_cast<const float4v*>(p.part + t * parts * (BT * BT) + BT * r + c);
-    float4v sum[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll 4
-    for (int k = 1; k < parts; ++k)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) sum[v] += x[k * (BT * BT / 4) + v];
-    if constexpr (OUT_F32) {
-        float4v* o = reinterpret_cast<float4v*>(static_cast<float*>(p.out) + (r0 + r) * p.C + c0 + c);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) o[v] = sum[v];
-    } else {
-        u32x4* o = reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (r0 + r) * p.C + c0 + c);
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-            o[v] = u32x4{pack_bf16x2(sum[2 * v][0], sum[2 * v][1]), pack_bf16x2(sum[2 * v][2], sum[2 * v][3]),
-                         pack_bf16x2(sum[2 * v + 1][0], sum[2 * v + 1][1]), pack_bf16x2(sum[2 * v + 1][2], sum[2 * v + 1][3])};
-    }
 }
 
 // 256 x CW output tiles: 8 waves, two per SIMD.  CW = 256: waves of 128 x 64 (NI =
@@ -695,151 +645,62 @@ __global__ __launch_bounds__(512, 1) void k_gemm_b128_wide(B128Args p) {
     }
 }
 
-// A row or two an expert: the weights' bytes bound the product, so they go from
-// memory straight to the registers of the one wave that uses them.  A workgroup
-// takes 16 rows of an expert and 64 columns; its four waves take every fourth
-// block of the reduction, each with the next THIN_DEPTH ones' operands in flight,
-// and add up in LDS in wave order.  64 rows over 32 experts (26 with rows) of
-// 4096 x 7168: 133 us, 5.8 TB/s; non-temporal weight loads 156 us.
-constexpr int TR = 16, TC = 64;
-constexpr int THIN_DEPTH = 2;  // (1 the same, 4: 139 us in the case below)
-template <bool OUT_F32>
-__global__ __launch_bounds__(256, 2) void k_gemm_b128_thin(B128Args p) {
-    __shared__ __align__(16) float4v s_sum[4][4][64];  // [wave][column group][lane]
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int CT = (int)((p.C + TC - 1) / TC);
-    const RowTile f = find_row_tile<TR>(p, blockIdx.x / CT, lane);
-    if (f.e < 0) return;
-    const int e = f.e, c0 = TC * (int)(blockIdx.x % CT);
-    const int rows = __builtin_amdgcn_readfirstlane((int)min((int64_t)TR, f.end - f.row0));
-    const int cols = __builtin_amdgcn_readfirstlane((int)min((int64_t)TC, p.C - c0));
-    const uint32_t ld = __builtin_amdgcn_readfirstlane((uint32_t)p.R), M = __builtin_amdgcn_readfirstlane((uint32_t)p.M);
-    const uint32_t len = e < p.E ? ld : 0u;
-    const int nb = (int)((len + 127) / 128);
-    const int64_t we = e < p.E ? e : 0;
-    const float* bs = uniform_ptr(p.bs + we * p.bs_e + (int64_t)(c0 / 128) * p.bs_c);
-    const __amdgpu_buffer_rsrc_t ra = rsrc_n(uniform_ptr(p.a + f.row0 * p.R), (uint32_t)rows * ld);
-    const __amdgpu_buffer_rsrc_t rb = rsrc_n(uniform_ptr(p.b + (we * p.C + c0) * p.R), (uint32_t)cols * ld);
-    const __amdgpu_buffer_rsrc_t rsa = rsrc_n(uniform_ptr(p.as + f.row0), 0x7FFFFFFFu);
-    const int lr = lane & 15, q = lane >> 4;
-    const uint32_t at = (uint32_t)lr * ld;
-    struct Stage {
-        u32x4 a[2], b[4][2];
-        float sa, sw;
-    };
-    auto load = [&](Stage& s, int blk) {
-        const uint32_t k0 = 128u * (uint32_t)blk + 16u * (uint32_t)q, k1 = k0 + 64u;
-        const uint32_t o0 = k0 < len ? at + k0 : OOB, o1 = k1 < len ? at + k1 : OOB;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s.b[j][0] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(o0 + (uint32_t)(16 * j) * ld), 0, 0);
-            s.b[j][1] = __builtin_amdgcn_raw_buffer_load_b128(rb, (int)(o1 + (uint32_t)(16 * j) * ld), 0, 0);
-        }
-        s.a[0] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)o0, 0, 0);
-        s.a[1] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)o1, 0, 0);
-        s.sa = __uint_as_float(buf_load4(rsa, lr < (blk < nb ? rows : 0) ? 4u * ((uint32_t)blk * M + (uint32_t)lr) : OOB));
-        s.sw = bs[(blk < nb ? blk : 0) * p.bs_b];
-    };
-    auto frag = [](const u32x4& x, const u32x4& y) {
-        return int8v{(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
-    };
-    float4v acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = float4v{0.0f, 0.0f, 0.0f, 0.0f};
-    auto use = [&](const Stage& s) {
-        const int8v fa = frag(s.a[0], s.a[1]);
-        const float sc = s.sa * s.sw;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4v d = b128_mfma(frag(s.b[j][0], s.b[j][1]), fa);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) acc[j][v] = fmaf(d[v], sc, acc[j][v]);
-        }
-    };
-    Stage s[THIN_DEPTH];
-    if (nb > 0) {
-#pragma unroll
-        for (int i = 0; i < THIN_DEPTH; ++i) load(s[i], wave + 4 * i);
-        for (int blk = wave; blk < nb; blk += 4 * THIN_DEPTH) {
-#pragma unroll
-            for (int i = 0; i < THIN_DEPTH; ++i) {
-                use(s[i]);  // zeros past the last block
-                load(s[i], blk + 4 * (THIN_DEPTH + i));
-            }
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[wave][j][lane] = acc[j];
-    __syncthreads();
-    float4v r = s_sum[0][wave][lane];
-#pragma unroll
-    for (int w = 1; w < 4; ++w) r += s_sum[w][wave][lane];
-    const __amdgpu_buffer_rsrc_t ro = make_rsrc(
-        uniform_ptr(static_cast<char*>(p.out) + (f.row0 * p.C + c0) * (OUT_F32 ? 4 : 2)), 0x7FFFFFFFu);
-    const int c = 16 * wave + 4 * q;
-    const uint32_t o = (lr < rows && c < cols) ? ((uint32_t)lr * (uint32_t)p.C + (uint32_t)c) * (OUT_F32 ? 4u : 2u) : OOB;
-    if constexpr (OUT_F32)
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, r), ro, (int)o, 0, 0);
-    else
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3])}, ro, (int)o, 0, 0);
-}
-
 namespace {
 
 constexpr int64_t kMaxOffset = (int64_t)1 << 31;  // 32-bit buffer offsets
+constexpr int64_t MAX_GRID = (int64_t)1 << 24;    // workgroups of 256 threads (of 512: half as many)
 
 bool al(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Most row tiles of TM rows that E experts and the rows past them can need.
 int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M : E + 1); }
 
-// Which form runs, by the call's sizes:
-//  - at most THIN_ROWS rows an expert on average (not wgrad): 16 x 64 tiles.  32
-//    experts of 4096 x 7168: 64 rows 133 us against 146 of the 256 x 256 tiles;
-//    128 rows 165 against 158 (148 with the streamed weights below).
-//  - 128 x 128 tiles in parts along the reduction, as many as run at once
-//    (SPLIT_AT_ONCE) and have room in the workspace, of at least SPLIT_STAGES blocks,
-//    where few tiles have a long one: 8 rows over 2 experts of 304 x 5696 14 us
-//    against 35 in one part, 256 over 4 of 2048 x 7168 24 against 44, 1375 over 13 of
-//    336 x 7104 24 against 43; wgrad of 17618 rows, 2 experts of 272 x 416 25
-//    against 98, 32768 rows, 8 experts of 512 x 512 47 against 99.  From SPLIT_FROM
-//    blocks on (the join takes 5 us and its bytes: 20 blocks 16.4 against 19.2, at
-//    most the same below), SPLIT_LONG where the tiles alone take more than a quarter
-//    of the chip's places (512 rows over 2 experts of 3584 x 4096, 32 blocks, 34
-//    against 29, but 1024 over 4 of 2048 x 7168, 56 blocks, 40 against 45).  wgrad counts twice the experts' average
-//    blocks, as the routing's skew puts most of them on a few.
-//  - 128 x 128 tiles while about all of them run at once, two to a compute unit
-//    (an expert's last tile counts half): 8 experts of 4096 x 7168, 1024 rows 49 to
-//    63 us (even experts to the routing's skew) against 68 to 85, 2048 rows 81 to
-//    113 against 99 to 86 (7/8 of those places from CROWDED_ROWS rows an expert on,
-//    where the big tiles are fuller and the count is an average: 3083 skewed rows over
-//    28 experts of 1616 x 4160, 494 tiles, 70 us against 51, 3434 over 17 of 1792 x
-//    976, 483, 26 against 19, but 1536 even rows over 8 of 4096 x 7168, 512, 75
-//    against 90; over random sizes of this kind the big tiles take 9% less);
-//    and up to TILE_ROWS rows an expert, where most tiles are an expert's last: 32
-//    experts of 4096 x 7168, 1024 rows 196 us against 222, 2048 rows 213 against
-//    231, 4096 rows 280 against 283.  Half as many where the reduction is shorter
-//    than LONG_R, as the big tiles' stores go out beside products: 32 experts of
-//    7168 x 2048, 1024 rows 95 to 110 us against 95 to 104, 2048 rows 107 to 118
-//    against 99 to 113; 64 experts of 2048 x 2048, 2048 rows 48 to 56 against 45
-//    to 60, 4096 rows 51 to 64 against 47 to 66.
-//    Their weight loads are non-temporal where hardly a weight is read twice (up
-//    to STREAM_ROWS rows an expert), the weights do not fit the last-level cache
-//    from one call to the next and their rows are whole lines: 32 experts of
-//    4096 x 7168, 128 rows 148 us against 159, 512 rows 180 against 192, but 2048
-//    rows 225 against 211, and 32 experts of 1424 x 2000 (91 MB), 128 rows 27
-//    against 20.
+// Which form runs, by the call's sizes (us; tiles are counted from the average
+// expert, whose last one counts half, as the host does not know the others):
+//  - 32 x 32 tiles up to FEW_TILES tiles of 64 x 64, which would leave most compute
+//    units idle, each at the rate of the lines its first-level cache has in flight: 8
+//    rows over 2 experts of 304 x 5696 14 against 18, 219 over 19 of 416 x 5408 21
+//    against 23, but 168 over 4 of 2912 x 5536 (184 tiles) 32 against 26.  wgrad up
+//    to FEW_TILES_WGRAD: 25434 rows, 2 experts of 1040 x 224, 46 against 66, but 17129
+//    over 5 of 160 x 1584 (375) 29 against 22.
+//  - 64 x 64 tiles up to SOME_TILES of them: 862 rows over 3 experts of 2176 x 6128 40
+//    against 49 of 128 x 128 tiles, 12113 over 3 of 160 x 2368 18 against 20, but 1140
+//    over 10 of 2016 x 2512 (704) 31 against 27.  wgrad up to SOME_TILES_WGRAD: 28890
+//    rows, 14 experts of 768 x 736, 59 against 86, but 2889 over 2 of 1056 x 5808
+//    (3094) 47 against 43 and 39 of 256 x 256 tiles; below it a few long experts lose:
+//    9852 rows of one of 3552 x 1488 101 against 89.
+//  - 64 x 64 tiles also up to SOME_ROWS rows an expert, where most tiles are an expert's
+//    last: 1024 rows over 32 experts of 2048 x 2048 35 (skewed; even 30) against 40 (32),
+//    1536 over 48 of 1024 x 4096 53 (51) against 58 (54), 128 over 32 of 4096 x 7168 162
+//    against 163, but 1024 214 (171) against 197 (167).  Their weight loads are
+//    non-temporal where hardly a weight is read twice (up to STREAM_ROWS rows an expert),
+//    the weights do not fit the last-level cache from one call to the next and their rows
+//    are whole lines: 64 rows over 32 experts of 4096 x 7168 120 against 133, 128 146
+//    against 162, 512 183 against 196, but 2048 304 against 260.
 //  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
 //    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
-//    x 2000 22 us against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
+//    x 2000 22 against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
 //    routing's skew would be 93 against 75 and 83, hence the margin of 1/8; none with
 //    FULL_ROWS rows an expert, where few tiles are an expert's last: 15921 rows of one
 //    expert of 512 x 1952, 250 tiles, 21 against 29 and 33, 19273 over 3 of 304 x 3472,
 //    229, 34 against 40 and 46, but 4051 over 12 of 1408 x 1184, 231, 25 against 20
-//    and 21.
+//    and 21, and 7559 over 6 of 960 x 6912, just 256, 88 against 62.
+//  - 128 x 128 tiles while about all of them run at once, two to a compute unit: 8
+//    experts of 4096 x 7168, 1024 rows 49 to 63 (even experts to the routing's skew)
+//    against 68 to 85, 2048 rows 81 to 113 against 99 to 86 (7/8 of those places from
+//    CROWDED_ROWS rows an expert on, where the big tiles are fuller and the count is an
+//    average: 3083 skewed rows over 28 experts of 1616 x 4160, 494 tiles, 70 against 51,
+//    3434 over 17 of 1792 x 976, 483, 26 against 19, but 1536 even rows over 8 of 4096 x
+//    7168, 512, 75 against 90; over random sizes of this kind the big tiles take 9%
+//    less); and up to TILE_ROWS rows an expert, where most tiles are an expert's last:
+//    32 experts of 4096 x 7168, 2048 rows 213 against 231.  Half as many where the
+//    reduction is shorter than LONG_R, as the big tiles' stores go out beside products:
+//    32 experts of 7168 x 2048, 2048 rows 107 to 118 against 99 to 113; 64 experts of
+//    2048 x 2048, 2048 rows 48 to 56 against 45 to 60, 4096 rows 51 to 64 against 47 to 66.
 //  - else 256 x 256 tiles.
-constexpr int64_t THIN_ROWS = 2;
+constexpr int64_t FEW_TILES = 128, FEW_TILES_WGRAD = 256;
+constexpr int64_t SOME_TILES = 576, SOME_TILES_WGRAD = 2048;
+constexpr int64_t SOME_ROWS = 32;
 constexpr int64_t TILE_ROWS = 64;
 constexpr int64_t LONG_R = 4096;
 constexpr int64_t STREAM_ROWS = 16;
@@ -847,19 +708,13 @@ constexpr int64_t TILES_AT_ONCE = 512;
 constexpr int64_t CROWDED_ROWS = 96;
 constexpr int64_t MID_AT_ONCE = 256;
 constexpr int64_t FULL_ROWS = 512;
-constexpr int64_t SPLIT_AT_ONCE = 512;
-constexpr int64_t SPLIT_STAGES = 6;
-constexpr int64_t SPLIT_FROM = 20;
-constexpr int64_t SPLIT_LONG = 48;
-constexpr int64_t SPLIT_TILES = 512;  // 32 MB of workspace
 constexpr int64_t LAST_LEVEL_CACHE = (int64_t)256 << 20;
 
-// Where the parts of split reductions start in the workspace.
 size_t plan_bytes(int E) { return (size_t)((plan_words(E + 1) * 4 + 255) / 256 * 256); }
 
 template <class K>
 bsq_status run(K kernel, int64_t grid, int threads, size_t lds, const B128Args& a, hipStream_t s) {
-    if (grid * threads >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
+    if (grid >= MAX_GRID || grid * threads >= (int64_t)1 << 32) return BSQ_ERR_UNSUPPORTED;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(threads), lds, s, a);
     return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
 }
@@ -879,32 +734,42 @@ bsq_status launch_wide(const B128Args& a, hipStream_t s) {
     return run(k_gemm_b128_wide<F32, WGRAD, CW>, (tiles + 255) / 256 * 256, 512, lds, a, s);
 }
 
+// Workgroups of k_gemm_b128_tile (forward: row tiles in groups of 8).
+template <bool WGRAD, int BT>
+int64_t tile_grid(const B128Args& a) {
+    return (WGRAD ? a.E * ((a.R + BT - 1) / BT) : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8) * ((a.C + BT - 1) / BT);
+}
+
+template <bool F32, bool WGRAD, int BT, int B_AUX>
+bsq_status launch_tile(B128Args a, bool even, hipStream_t s) {
+    a.even = even;
+    return run(k_gemm_b128_tile<F32, WGRAD, BT, B_AUX>, tile_grid<WGRAD, BT>(a), 256, 0, a, s);
+}
+
 template <bool F32, bool WGRAD>
-bsq_status launch_b128(B128Args a, hipStream_t s) {
-    if constexpr (!WGRAD)
-        if (a.M <= THIN_ROWS * a.E)
-            return run(k_gemm_b128_thin<F32>, max_row_tiles(a.M, a.E, TR) * ((a.C + TC - 1) / TC), 256, 0, a, s);
-    const int64_t ct = (a.C + BT - 1) / BT, live = a.M < a.E ? a.M : a.E;
-    const int64_t tiles = WGRAD ? (int64_t)a.E * ((a.R + BT - 1) / BT) * ct : (2 * (a.M / BT) + live) * ct / 2;
-    const int64_t grid = WGRAD ? tiles : (max_row_tiles(a.M, a.E, BT) + 7) / 8 * 8 * ct;  // (row tiles in groups of 8)
-    a.even = tiles <= TILES_AT_ONCE;
-    const int64_t stages = WGRAD ? (a.M + 127) / 128 * (a.E > 1 ? 2 : 1) / a.E : (a.R + 127) / 128;
-    const int64_t parts = std::min({SPLIT_AT_ONCE / std::max(tiles, (int64_t)1), stages / SPLIT_STAGES, SPLIT_TILES / grid});
-    if (parts > 1 && stages >= (tiles > SPLIT_AT_ONCE / 4 ? SPLIT_LONG : SPLIT_FROM)) {
-        hipLaunchKernelGGL((k_gemm_b128_tile<true, WGRAD, 0, true>), dim3((unsigned)grid, (unsigned)parts), dim3(256), 0, s, a);
-        if (hipGetLastError() != hipSuccess) return BSQ_ERR_HIP;
-        hipLaunchKernelGGL((k_gemm_b128_join<F32, WGRAD>), dim3((unsigned)(4 * grid)), dim3(256), 0, s, a, (int)parts);
-        return hipGetLastError() == hipSuccess ? BSQ_OK : BSQ_ERR_HIP;
-    }
-    if constexpr (!WGRAD)
-        if (tiles > TILES_AT_ONCE / 2 && (2 * (a.M / WT) + live) * ct / 2 <= (a.M < FULL_ROWS * a.E ? MID_AT_ONCE * 7 / 8 : MID_AT_ONCE))
+bsq_status launch_b128(const B128Args& a, hipStream_t s) {
+    // tiles of TM x TN (forward: an expert's last one counts half)
+    auto tiles = [&](int64_t TM, int64_t TN) {
+        const int64_t ct = (a.C + TN - 1) / TN;
+        return WGRAD ? a.E * ((a.R + TM - 1) / TM) * ct : (2 * (a.M / TM) + std::min(a.M, (int64_t)a.E)) * ct / 2;
+    };
+    const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128);
+    if (t64 <= (WGRAD ? FEW_TILES_WGRAD : FEW_TILES)) return launch_tile<F32, WGRAD, 32, 0>(a, true, s);
+    if constexpr (WGRAD) {
+        if (t64 <= SOME_TILES_WGRAD) return launch_tile<F32, true, 64, 0>(a, true, s);
+        return t128 > TILES_AT_ONCE ? launch_wide<F32, true, 256>(a, s) : launch_tile<F32, true, 128, 0>(a, true, s);
+    } else {
+        if (t64 <= SOME_TILES || (a.M <= SOME_ROWS * a.E && tile_grid<false, 64>(a) < MAX_GRID)) {
+            const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
+            return stream ? launch_tile<F32, false, 64, 2>(a, true, s) : launch_tile<F32, false, 64, 0>(a, true, s);
+        }
+        if (t128 > TILES_AT_ONCE / 2 && tiles(256, 128) <= (a.M < FULL_ROWS * a.E ? MID_AT_ONCE * 7 / 8 : MID_AT_ONCE))
             return launch_wide<F32, false, 128>(a, s);
-    const int64_t at_once = WGRAD || a.M < CROWDED_ROWS * a.E ? TILES_AT_ONCE : TILES_AT_ONCE * 7 / 8;
-    if (tiles > at_once && (WGRAD || a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)) return launch_wide<F32, WGRAD, 256>(a, s);
-    if constexpr (WGRAD) return run(k_gemm_b128_tile<F32, true, 0>, grid, 256, 0, a, s);
-    const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
-    return stream ? run(k_gemm_b128_tile<F32, false, 2>, grid, 256, 0, a, s)
-                  : run(k_gemm_b128_tile<F32, false, 0>, grid, 256, 0, a, s);
+        if (t128 > (a.M < CROWDED_ROWS * a.E ? TILES_AT_ONCE : TILES_AT_ONCE * 7 / 8) &&
+            a.M > (a.R < LONG_R ? TILE_ROWS / 2 : TILE_ROWS) * a.E)
+            return launch_wide<F32, false, 256>(a, s);
+        return launch_tile<F32, false, 128, 0>(a, t128 <= TILES_AT_ONCE, s);
+    }
 }
 
 template <bool WGRAD>
@@ -919,7 +784,7 @@ extern "C" {
 
 size_t bsq_grouped_gemm_fp8b128_workspace_size(int32_t num_experts) {
     if (num_experts < 1 || num_experts > bsq::MAX_EXPERTS) return 0;
-    return bsq::plan_bytes(num_experts) + (size_t)(bsq::SPLIT_TILES * bsq::BT * bsq::BT * 4);
+    return bsq::plan_bytes(num_experts);
 }
 
 bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
@@ -942,9 +807,8 @@ bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_s
     if (m_total == 0) return BSQ_OK;
     const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
     int32_t* err = static_cast<int32_t*>(workspace) + bsq::PLAN_ERR;
-    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     const bsq::B128Args a{a_codes, a_scale, w_codes, w_scale, offsets, num_experts, m_total, k, n, 0,
-                          nb * kb, kb, 1, y, err, part, 0};
+                          nb * kb, kb, 1, y, err, 0};
     return bsq::launch_b128<false>(a, y_dtype == BSQ_F32, stream);
 }
 
@@ -977,16 +841,15 @@ bsq_status bsq_grouped_gemm_fp8b128_bwd(const uint8_t* dy_codes, const float* dy
     if (workspace_bytes < bsq_grouped_gemm_fp8b128_workspace_size(num_experts)) return BSQ_ERR_WORKSPACE_TOO_SMALL;
     const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
     int32_t* err = static_cast<int32_t*>(workspace) + bsq::PLAN_ERR;
-    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + bsq::plan_bytes(num_experts));
     if (dg && m_total > 0) {
         const bsq::B128Args a{dy_codes, dy_scale, wt_codes, w_scale, offsets, num_experts, m_total, n, k, 0,
-                              nb * kb, 1, kb, dx, err, part, 0};
+                              nb * kb, 1, kb, dx, err, 0};
         const bsq_status st = bsq::launch_b128<false>(a, dx_dtype == BSQ_F32, stream);
         if (st != BSQ_OK) return st;
     }
     if (wg) {
         const bsq::B128Args a{dyt_codes, dyt_scale, xt_codes, xt_scale, offsets, num_experts, m_total, n, k, P,
-                              0, 0, 0, dw, err, part, 0};
+                              0, 0, 0, dw, err, 0};
         return bsq::launch_b128<true>(a, dw_dtype == BSQ_F32, stream);
     }
     return BSQ_OK;
