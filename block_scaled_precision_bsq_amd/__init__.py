@@ -9,6 +9,7 @@ importing this package fails if the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -104,22 +105,23 @@ def _empty(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-# Workspaces up to this size come out of the outputs' allocation, which they
-# then share the life of.
-_SMALL = 1 << 16
+# Bytes of outputs and workspace up to which one allocation holds all of them (an
+# allocation apiece costs such a call more time than its kernel).
+_SMALL = 1 << 14
 
 
-def _carve(stream, dtype, device, sizes, scratch=None):
-    """Dense 1-D buffers of the given lengths out of one allocation (4-byte
-    types): for a call whose outputs live and die together, an allocation
-    apiece costs more time than its kernel.  With ``scratch`` bytes also the
-    address of that much workspace (last), on 256 bytes."""
-    if scratch is None:
-        return _empty(stream, (sum(sizes),), dtype, device).split_with_sizes(sizes)
+def _carve(stream, dtype, device, sizes, scratch=0):
+    """Dense 1-D tensors of the given lengths out of one allocation (4-byte types),
+    and the address of ``scratch`` bytes of workspace on 256 bytes (last, where
+    wanted).  Each is a tensor of its own (.data): an in-place change of one, an
+    all-reduce of counts say, does not count as a change of another that
+    autograd has saved."""
+    if not scratch:
+        return [t.data for t in _empty(stream, (sum(sizes),), dtype, device).split_with_sizes(sizes)]
     n = sum(sizes)
     base = _empty(stream, (n + scratch // 4 + 64,), dtype, device)
-    *out, rest = base.split_with_sizes((*sizes, scratch // 4 + 64))
-    return *out, (base.data_ptr() + 4 * n + 255) & -256
+    *out, _ = base.split_with_sizes((*sizes, scratch // 4 + 64))
+    return [t.data for t in out] + [(base.data_ptr() + 4 * n + 255) & -256]
 
 
 def _ptr(t):
@@ -488,7 +490,7 @@ def _shaped(t, name, dtypes, shape, dev):
 
 def _scratch(need, workspace, dev, stream):
     if workspace is None:
-        return _empty(stream, (need,), dtype=torch.uint8, device=dev)
+        return _empty(stream, (max(need, 1),), dtype=torch.uint8, device=dev)  # (0: sizes that the call refuses)
     _dev(workspace, "workspace", (workspace.dtype,))
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on {dev}")
@@ -527,15 +529,17 @@ def bsq_moe_route(logits, top_k, bias=None, mask=None, normalize=True, scale=1.0
     if mask is not None:
         _shaped(mask, "mask", (torch.uint8, torch.bool), (T,), dev)
     need = bsq_moe_route_workspace_size(T, E)
-    sizes = T * top_k, E + 1, T * top_k + T + 1
-    if workspace is None and need <= _SMALL:
-        ids, counts, floats, ws = _carve(stream, torch.int32, dev, sizes, need)
+    sizes = T * top_k, T * top_k, T, E + 1, 1
+    if workspace is None and 0 < need <= _SMALL - 4 * sum(sizes):
+        ids, weights, lse, counts, loss, ws = _carve(stream, torch.float32, dev, sizes, need)
+        ids, weights, counts = ids.view(torch.int32).view(T, top_k), weights.view(T, top_k), counts.view(torch.int32)
     else:
-        ids, counts, floats = _carve(stream, torch.int32, dev, sizes)
-        workspace = _scratch(need, workspace, dev, stream)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(stream):  # (as _empty, once for all)
+            ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+            weights, lse, loss = (torch.empty(n, device=dev, dtype=torch.float32) for n in ((T, top_k), T, 1))
+            counts = torch.empty(E + 1, dtype=torch.int32, device=dev)
+            workspace = _scratch(need, workspace, dev, None)
         ws, need = _ptr(workspace), workspace.numel() * workspace.element_size()
-    weights, lse, loss = floats.view(torch.float32).split_with_sizes((T * top_k, T, 1))
-    ids, weights = ids.view(T, top_k), weights.view(T, top_k)
     _check("bsq_moe_route",
            _lib.bsq_moe_route(_ptr(logits), dt, T, E, ld, top_k, _ptr(bias), _ptr(mask), int(normalize),
                               scale, loss_coef, _ptr(ids), _ptr(weights), _ptr(lse), _ptr(counts), _ptr(loss), ws, need,
@@ -588,7 +592,8 @@ def bsq_moe_dispatch(expert_ids, num_experts, workspace=None, stream=None):
     dev = expert_ids.device
     need = bsq_moe_dispatch_workspace_size(T, K, num_experts)
     sizes = num_experts + 1, T * K, T * K
-    if workspace is None and need <= _SMALL:
+    # (the workspace of a larger call is a small part of the outputs)
+    if workspace is None and 0 < need <= max(_SMALL - 4 * sum(sizes), sum(sizes) // 2):
         offsets, row_index, slot, ws = _carve(stream, torch.int32, dev, sizes, need)
     else:
         offsets, row_index, slot = _carve(stream, torch.int32, dev, sizes)
