@@ -677,8 +677,8 @@ int64_t max_row_tiles(int64_t M, int E, int TM) { return M / TM + (M < E + 1 ? M
 //    the weights do not fit the last-level cache from one call to the next and their rows
 //    are whole lines: 64 rows over 32 experts of 4096 x 7168 120 against 133, 128 146
 //    against 162, 512 183 against 196, but 2048 304 against 260.
-//  - 256 x 128 tiles where 128 x 128 ones need the second place of some compute
-//    units and these only the first (not wgrad): 3001 rows over 12 experts of 1424
+//  - wgrad beyond: 256 x 256 tiles.  256 x 128 ones where 128 x 128 ones need the
+//    second place of some compute units and these only the first: 3001 rows over 12 experts of 1424
 //    x 2000 22 against 29 and 30; 8 experts of 4096 x 7168, 1536 rows with the
 //    routing's skew would be 93 against 75 and 83, hence the margin of 1/8; none with
 //    FULL_ROWS rows an expert, where few tiles are an expert's last: 15921 rows of one
@@ -753,12 +753,12 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
         const int64_t ct = (a.C + TN - 1) / TN;
         return WGRAD ? a.E * ((a.R + TM - 1) / TM) * ct : (2 * (a.M / TM) + std::min(a.M, (int64_t)a.E)) * ct / 2;
     };
-    const int64_t t64 = tiles(64, 64), t128 = tiles(128, 128);
+    const int64_t t64 = tiles(64, 64);
     if (t64 <= (WGRAD ? FEW_TILES_WGRAD : FEW_TILES)) return launch_tile<F32, WGRAD, 32, 0>(a, true, s);
     if constexpr (WGRAD) {
-        if (t64 <= SOME_TILES_WGRAD) return launch_tile<F32, true, 64, 0>(a, true, s);
-        return t128 > TILES_AT_ONCE ? launch_wide<F32, true, 256>(a, s) : launch_tile<F32, true, 128, 0>(a, true, s);
+        return t64 <= SOME_TILES_WGRAD ? launch_tile<F32, true, 64, 0>(a, true, s) : launch_wide<F32, true, 256>(a, s);
     } else {
+        const int64_t t128 = tiles(128, 128);
         if (t64 <= SOME_TILES || (a.M <= SOME_ROWS * a.E && tile_grid<false, 64>(a) < MAX_GRID)) {
             const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
             return stream ? launch_tile<F32, false, 64, 2>(a, true, s) : launch_tile<F32, false, 64, 0>(a, true, s);
