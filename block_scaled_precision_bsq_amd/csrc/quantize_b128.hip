@@ -276,8 +276,8 @@ __global__ __launch_bounds__(256) void k_quantize_b128_cols(const uint16_t* __re
 }
 
 // Weights: one workgroup per 128 x 128 block of one expert.  32 x 4096 x 7168:
-// 674 us, 5.6 TB/s, the copy rate (ordinary loads and stores 696 us; another
-// card takes 706).
+// 706 us, 5.3 TB/s, where a device copy of 2 GiB moves 4.9 to 5.1 (another card 674,
+// and there 696 with ordinary loads and stores).
 template <bool TRANS>
 __global__ __launch_bounds__(256) void k_quantize_b128_weights(const uint16_t* __restrict__ w, int n, int k,
                                                                int64_t ld, uint8_t* __restrict__ codes,

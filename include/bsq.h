@@ -418,6 +418,7 @@ bsq_status bsq_grouped_gemm_w4a16(const void* x_bf16, const uint8_t* w_codes, co
  *   workspace >= bsq_moe_route_workspace_size(tokens, num_experts) bytes,
  *   256-byte aligned; scratch.
  * Sums over tokens run in a fixed order (repeated runs give the same bits).
+ * A probability below 2^-126 counts as 0.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes, alignment), WORKSPACE_TOO_SMALL, HIP.
  */
 bsq_status bsq_moe_route(const void* logits, bsq_dtype dtype, int64_t tokens, int32_t num_experts, int64_t ld,
