@@ -160,11 +160,10 @@ __global__ __launch_bounds__(256, 2) void k_gemm_b128_tile(B128Args p) {
     uint32_t tile = blockIdx.x;  // (grids stay below 2^24 workgroups)
     if constexpr (!WGRAD) {
         // An XCD gets every eighth workgroup.  Either eight row tiles sweep the column
-        // tiles together, each on its XCD, or (p.even: where all tiles run at once, and
-        // the smaller tiles) an XCD takes an eighth of them, row by row: as many as the
-        // others do (17 row tiles of 11 column tiles 36 us against 55 the other way,
-        // where one XCD gets three of them and another two; many rounds of 128 x 128
-        // tiles up to 5% slower).
+        // tiles together, each on its XCD, or (p.even) an XCD takes an eighth of them,
+        // row by row: as many as the others do (17 row tiles of 11 column tiles 36 us
+        // against 55 the other way, where one XCD gets three of them and another two;
+        // many rounds of 128 x 128 tiles up to 5% slower).
         bool on = true;
         const RowTile f = pick_row_tile<BT, true>(p, lane, [&](int64_t all) {
             if (p.even) {
@@ -754,14 +753,19 @@ bsq_status launch_b128(const B128Args& a, hipStream_t s) {
         return WGRAD ? a.E * ((a.R + TM - 1) / TM) * ct : (2 * (a.M / TM) + std::min(a.M, (int64_t)a.E)) * ct / 2;
     };
     const int64_t t64 = tiles(64, 64);
-    if (t64 <= (WGRAD ? FEW_TILES_WGRAD : FEW_TILES)) return launch_tile<F32, WGRAD, 32, 0>(a, true, s);
+    // the smaller tiles in even shares where one scan of the experts counts them all (16
+    // rows of one expert of 7168 x 2816 12 us against 21, 512 over 2 of 3584 x 4096 22
+    // against 33; but 384 over 384 of 2048 x 1024 97 against 78, 1024 over 1024 of 512 x
+    // 512 101 against 72)
+    const bool even = a.E < 64;
+    if (t64 <= (WGRAD ? FEW_TILES_WGRAD : FEW_TILES)) return launch_tile<F32, WGRAD, 32, 0>(a, even, s);
     if constexpr (WGRAD) {
-        return t64 <= SOME_TILES_WGRAD ? launch_tile<F32, true, 64, 0>(a, true, s) : launch_wide<F32, true, 256>(a, s);
+        return t64 <= SOME_TILES_WGRAD ? launch_tile<F32, true, 64, 0>(a, even, s) : launch_wide<F32, true, 256>(a, s);
     } else {
         const int64_t t128 = tiles(128, 128);
         if (t64 <= SOME_TILES || (a.M <= SOME_ROWS * a.E && tile_grid<false, 64>(a) < MAX_GRID)) {
             const bool stream = a.M <= STREAM_ROWS * a.E && a.R % 128 == 0 && a.E * a.C * a.R > LAST_LEVEL_CACHE;
-            return stream ? launch_tile<F32, false, 64, 2>(a, true, s) : launch_tile<F32, false, 64, 0>(a, true, s);
+            return stream ? launch_tile<F32, false, 64, 2>(a, even, s) : launch_tile<F32, false, 64, 0>(a, even, s);
         }
         if (t128 > TILES_AT_ONCE / 2 && tiles(256, 128) <= (a.M < FULL_ROWS * a.E ? MID_AT_ONCE * 7 / 8 : MID_AT_ONCE))
             return launch_wide<F32, false, 128>(a, s);
