@@ -670,7 +670,7 @@ def bsq_moe_combine_bwd(dy, ye, slot, weights=None, offsets=None, m_total=None, 
 
 def bsq_quantize_fp8b128(x, row_index=None, offsets=None, rows_form=True, row=None, t=None, stream=None):
     """FP8B128 of bf16 ``x`` [src_rows, cols], or of x[row_index] (i32; out-of-range
-    indices give zero rows).  Returns (row, t): row = (codes u8 [rows, cols], scale
+    indices give zero rows); a block with an infinity or a NaN gets a NaN scale.  Returns (row, t): row = (codes u8 [rows, cols], scale
     f32 [ceil(cols/128), rows]), or None with rows_form=False; t = the
     token-column form (t_codes u8 [cols, P], t_scale f32 [P/128, cols]) where
     ``offsets`` (i32 [groups + 1]) is given, else None."""
@@ -747,7 +747,8 @@ def _out(t, name, dtype, shape, dev, stream):
 def bsq_grouped_gemm_fp8b128_fwd(a_q, w_q, offsets, y_dtype=BSQ_BF16, y=None, workspace=None, stream=None):
     """Forward grouped GEMM on FP8B128 operands: a_q = (codes [m_total, k], scale)
     of the expert-sorted activations in row form, w_q = (codes [E*n, k], scale [E,
-    ceil(n/128), ceil(k/128)]) of the weights.  Returns y [m_total, n]."""
+    ceil(n/128), ceil(k/128)]) of the weights.  Returns y [m_total, n]; a row's bits do
+    not depend on the other rows."""
     a_codes, a_scale = a_q
     w_codes, w_scale = w_q
     _dev(a_codes, "a codes", (torch.uint8,))

@@ -12,7 +12,7 @@
 // counting launch and a placing launch, whose workgroups each add up the
 // counts before them (a few hundred bytes per workgroup and expert, from L2)
 // instead of waiting for a third launch in between.  131072 choices of 384
-// experts: 3.0 and 8.1 us, bound by dependent steps (the counts, a scan, one
+// experts: 3.2 and 8.1 us, bound by dependent steps (the counts, a scan, one
 // counter per rank), not by their 1.5 MB; 128 choices in 3.6 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

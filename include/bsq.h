@@ -507,7 +507,8 @@ bsq_status bsq_moe_combine_bwd(const void* dy, bsq_dtype dtype, int64_t tokens, 
  * (not wanted).  offsets/num_groups (device, as for BSQ_COLWISE_T) are needed
  * for the token columns; rows past offsets[num_groups] are in no column.  With
  * both forms one read serves both, and offsets[0] must be 0.
- *   x_bf16 [src_rows][ld_x] 16-byte aligned, ld_x % 8 == 0; cols % 16 == 0.
+ *   x_bf16 [src_rows][ld_x] 16-byte aligned, ld_x % 8 == 0; cols % 16 == 0, cols
+ *   <= 2^22, rows <= 2^27; for the token columns P / 128 <= 65535, ld_x < 2^23.
  * bsq_quantize_fp8b128_weights -- w_bf16 [E*n][ld_w]; n % 16 == 0, k % 16 == 0;
  * codes_t may be NULL.
  * Errors: INVALID_ARG, UNSUPPORTED, HIP.
@@ -541,7 +542,9 @@ bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts,
  * this make the call do no work (bsq_debug_status on the workspace reports 1).
  * workspace >= bsq_grouped_gemm_fp8b128_workspace_size(num_experts) bytes,
  * 256-byte aligned; scratch.
- * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, HIP.
+ * Errors: INVALID_ARG, UNSUPPORTED (multiples, alignment, more than 4096 experts,
+ *   sizes beyond the kernels' 32-bit offsets: 256 rows of codes and of f32 outputs,
+ *   one operand's scales; 2^24 tiles), WORKSPACE_TOO_SMALL, HIP.
  */
 bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
                                         const float* w_scale, const int32_t* offsets, int32_t num_experts,
