@@ -544,7 +544,7 @@ bsq_status bsq_quantize_fp8b128_weights(const void* w_bf16, int32_t num_experts,
  * 256-byte aligned; scratch.
  * Errors: INVALID_ARG, UNSUPPORTED (multiples, alignment, more than 4096 experts,
  *   sizes beyond the kernels' 32-bit offsets: 256 rows of codes and of f32 outputs,
- *   one operand's scales; 2^24 tiles), WORKSPACE_TOO_SMALL, HIP.
+ *   one operand's scales; 2^23 tiles), WORKSPACE_TOO_SMALL, HIP.
  */
 bsq_status bsq_grouped_gemm_fp8b128_fwd(const uint8_t* a_codes, const float* a_scale, const uint8_t* w_codes,
                                         const float* w_scale, const int32_t* offsets, int32_t num_experts,
