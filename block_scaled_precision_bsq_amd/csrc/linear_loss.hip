@@ -32,6 +32,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "../../include/bsq.h"
 #include "device_common.h"
@@ -68,6 +69,7 @@ struct HeadArgs {
     int64_t ldx;             // bytes
     int64_t Hp, Tp;
     float scale;
+    float far_key;           // 2^(far - 20) of the pairs
     Live live;
     // rows (not direct)
     const int32_t* count;    // rows with a target
@@ -309,14 +311,18 @@ __global__ __launch_bounds__(256) void k_lists(ListArgs a) {
 
 // --------------------------------------------------------------- the logits' tiles
 
-// A part of a row's sum of exponentials is a pair (R, s): s = sum 2^(kappa z - R), kappa = scale
-// log2(e), z unscaled, R the whole number next to the part's largest kappa z (NOTHING where
-// there is none).  One rounding gives an exponent's argument, whatever the size of z, and merging
-// two parts is exact but for the addition.
-constexpr float NOTHING = -3e38f;
+// A part of a row's sum of exponentials is a pair (2^-20 R, s): s = sum 2^(kappa z - R), kappa = scale
+// log2(e), z unscaled, R the whole number next to the part's largest kappa z (NOTHING in its place where
+// there is none).  One rounding gives an exponent's argument, and merging two parts is exact but for the addition.
+// Where the largest kappa z is beyond FAR in size, the rounding of R itself, more than 32, is too much for an exponent, and
+// different z are 64 or more apart (2^-24 of their size).  There s = sum 2^(kappa (z - m)) with m the largest z, which is how
+// many are equal to it, and R is 2^f m, 2^f being the least power of two from kappa on: exact, beyond FAR as well, and of
+// different m still 64 or more apart.  (R is held as 2^-20 of it, which every finite m leaves in binary32 up to a scale of
+// 2^19.)  Logits of -1e10 and the lowest finite values, which mask parts of a vocabulary, are of this kind.
+constexpr float NOTHING = -3e38f, FAR = 1073741824.0f, KEY = 1.0f / (1 << 20), MOST = 3.40282347e38f;
 __device__ __forceinline__ float2 merge(float2 a, float2 b) {
     const float r = max_num(a.x, b.x);
-    auto scaled = [&](float2 x) { return ldexpf(x.y, (int)max_num(x.x - r, -512.0f)); };
+    auto scaled = [&](float2 x) { return ldexpf(x.y, (int)(max_num(x.x - r, -512.0f * KEY) * (1 / KEY))); };
     return make_float2(r, scaled(a) + scaled(b));
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -325,18 +331,27 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 // The pair of 16 values.
-__device__ __forceinline__ float2 pair16(const float (&x)[16], float kappa) {
+__device__ __forceinline__ float2 pair16(const float (&x)[16], float kappa, float far_key) {
     const float m = max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(max3(x[5], x[6], x[7]), x[8], x[9]),
                          max3(max3(x[10], x[11], x[12]), max3(x[13], x[14], x[15]), x[15]));
-    const float r = max_num(__builtin_rintf(m * kappa), NOTHING);
-    float e[16];
+    const float y = __builtin_rintf(m * kappa), r = max_num(y, NOTHING);
+    float e[16], key = max_num(y * KEY, NOTHING);
 #pragma unroll
-    for (int v = 0; v < 16; ++v) e[v] = __builtin_amdgcn_exp2f(fmaf(x[v], kappa, -r));
+    for (int v = 0; v < 16; ++v) e[v] = fmaf(x[v], kappa, -r);
+    const bool far = !(fabsf(r) <= FAR) && m > -INFINITY;
+    if (__builtin_expect(__ballot(far) != 0, 0)) {
+        const float k = kappa < MOST ? kappa : MOST;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) e[v] = far ? (x[v] - m) * k : e[v];
+        key = far ? fminf(fmaxf(m * far_key, NOTHING), -NOTHING) : key;
+    }
+#pragma unroll
+    for (int v = 0; v < 16; ++v) e[v] = __builtin_amdgcn_exp2f(e[v]);
 #pragma unroll
     for (int n = 1; n < 16; n *= 2)
 #pragma unroll
         for (int v = 0; v < 16; v += 2 * n) e[v] += e[v + n];
-    return make_float2(r, e[0]);
+    return make_float2(key, e[0]);
 }
 
 // The tile of workgroup wg: an XCD (every eighth workgroup) takes an eighth of them,
@@ -500,7 +515,7 @@ __global__ __launch_bounds__(64 * Loop::WAVES, 1) void k_logits(HeadArgs a) {
                 for (int i = 0; i < NP; ++i)
 #pragma unroll
                     for (int v = 0; v < 4; ++v) z = d == value(i, v) ? acc[i][j][v] : z;
-                if constexpr (LIST) a.logits[(int64_t)token[j] * a.K + slot] = a.scale * z;
+                if constexpr (LIST) a.logits[(int64_t)token[j] * a.K + slot] = z;  // (k_finish scales it)
                 else a.zat[q0 + 16 * (NQ * wq + j) + (lane & 15)] = z;
             });
             float2 u[NP / 4];
@@ -509,7 +524,7 @@ __global__ __launch_bounds__(64 * Loop::WAVES, 1) void k_logits(HeadArgs a) {
                 float x[16];
 #pragma unroll
                 for (int v = 0; v < 16; ++v) x[v] = acc[4 * n + v / 4][j][v & 3];
-                u[n] = pair16(x, kappa);
+                u[n] = pair16(x, kappa, a.far_key);
                 // with the lanes 16, then 32 away: the runs of 32 and of 64 columns
                 Pair32 pm = swap16(__float_as_uint(u[n].x)), ps = swap16(__float_as_uint(u[n].y));
                 u[n] = merge(make_float2(__uint_as_float(pm.a), __uint_as_float(ps.a)),
@@ -571,6 +586,8 @@ struct FinishArgs {
     const float2* part;
     int64_t blocks, Tp, T;
     float scale;
+    float far_unit;          // 2^(20 - far) of the pairs
+    double unit;             // scale / kappa
     Live live;
     const int32_t* pos;      // null: direct
     const float* zat;
@@ -578,8 +595,7 @@ struct FinishArgs {
     const int32_t* sslot;
     const float* sq;
     const uint16_t* tab;
-    const float* logits;
-    float *loss, *lse;
+    float *logits, *loss, *lse;
 };
 
 // LEAF columns a pair.  A workgroup takes TOK tokens; a thread the tree of 16 pairs of one token,
@@ -618,17 +634,32 @@ __global__ __launch_bounds__(256) void k_finish(FinishArgs a) {
         }
         __syncthreads();
     }
-    constexpr float LN2 = 0.693147181f;
-    const float ln = logf(all.y), lse = fmaf(all.x, LN2, ln);
+    constexpr float LN2 = 0.693147181f, LARGE = 65536.0f, HUGE_Z = 1e38f;
+    const float ln = logf(all.y);
+    // lse of a pair's (key, ln s).  Beyond LARGE the roundings of kappa and of R ln 2 would show beside ln s: 64 bits, or the
+    // largest logit as it is rounded by itself.
+    auto lse_of = [&](float key, float ln) {
+        const float R = key / KEY;
+        if (fabsf(R) > LARGE && key > NOTHING) {
+            const double top = fabsf(R) > FAR ? (double)(a.scale * (key * a.far_unit)) : R * a.unit;
+            return (float)(top + ln);
+        }
+        return fmaf(R, LN2, ln);
+    };
+    // lse - z of an unscaled logit, as the sum's own term of it was formed (its product with kappa may leave binary32, though)
+    auto loss_of = [&](float key, float ln, float z) {
+        const float R = key / KEY;
+        if (fabsf(R) > FAR && key > NOTHING) return ln - a.scale * (z - key * a.far_unit);
+        return fabsf(z * kappa) < HUGE_Z ? ln - LN2 * fmaf(z, kappa, -R) : lse_of(key, ln) - a.scale * z;
+    };
     if constexpr (!LIST) {
         if (g == 0 && t < a.T) {
-            a.lse[t] = pos >= 0 ? lse : -INFINITY;
-            // (as the sum's own term of the label was formed; not below 0 by a rounding)
-            const float loss = pos >= 0 ? ln - LN2 * fmaf(a.zat[pos], kappa, -all.x) : 0.0f;
-            a.loss[t] = loss < 0.0f ? 0.0f : loss;
+            a.lse[t] = pos >= 0 ? lse_of(all.x, ln) : -INFINITY;
+            const float loss = pos >= 0 ? loss_of(all.x, ln, a.zat[pos]) : 0.0f;
+            a.loss[t] = loss < 0.0f ? 0.0f : loss;  // (not below 0 by a rounding)
         }
     } else {
-        // a wave per token: its lanes share the list
+        // a wave per token: its lanes share the list, whose logits are unscaled so far
         __shared__ float s_m[TOK], s_l[TOK];
         if (g == 0) {
             s_m[tk] = all.x;
@@ -644,14 +675,16 @@ __global__ __launch_bounds__(256) void k_finish(FinishArgs a) {
             if (at >= 0) {
                 const int n = a.tab[u * (a.blocks + 1) + a.blocks];
                 for (int e = lane; e < n; e += 64) {
-                    const float q = a.sq[u * a.K + e], z = a.logits[u * a.K + a.sslot[u * a.K + e]];
-                    if (q != 0.0f) sum += q * (logf(q) + (s_l[k] - LN2 * fmaf(z, LOG2E, -s_m[k])));
+                    float* to = a.logits + u * a.K + a.sslot[u * a.K + e];
+                    const float q = a.sq[u * a.K + e], z = *to;
+                    *to = a.scale * z;
+                    if (q != 0.0f) sum += q * (logf(q) + loss_of(s_m[k], s_l[k], z));
                 }
             }
             sum = wave_sum_f32(sum);
             if (lane == 0 && u < a.T) {
                 a.loss[u] = at >= 0 ? sum : 0.0f;
-                a.lse[u] = at >= 0 ? fmaf(s_m[k], LN2, s_l[k]) : -INFINITY;
+                a.lse[u] = at >= 0 ? lse_of(s_m[k], s_l[k]) : -INFINITY;
             }
         }
     }
@@ -1290,8 +1323,13 @@ bsq_status run(const Call& c, void* workspace, size_t workspace_bytes, hipStream
         h.part = reinterpret_cast<float2*>(ws + p.part);
         h.zat = f32(p.zat);
         h.logits = c.logits;
+        const float kappa = c.scale * LOG2E;
+        const int far = (int)std::ceil(std::log2((double)c.scale * LOG2E));
+        h.far_key = std::ldexp(1.0f, far - 20);
+        const float far_unit = std::ldexp(1.0f, 20 - far);
+        const double unit = (double)c.scale / kappa;
         BSQ_TRY(list ? logits<false, true>(h, p, c.V, s) : logits<false, false>(h, p, c.V, s));
-        const FinishArgs f{h.part, p.blocks, p.Tp, c.T, c.scale, h.live, p.thin ? nullptr : i32(p.pos), h.zat, c.K, h.sslot, h.sq,
+        const FinishArgs f{h.part, p.blocks, p.Tp, c.T, c.scale, far_unit, unit, h.live, p.thin ? nullptr : i32(p.pos), h.zat, c.K, h.sslot, h.sq,
                            tab, c.logits, c.loss, c.lse};
         return list ? finish<true>(f, p.block, s) : finish<false>(f, p.block, s);
     }

@@ -562,6 +562,8 @@ size_t bsq_grouped_gemm_fp8b128_workspace_size(int32_t num_experts);
  * Losses at the output head, without its logits in memory.  With x [tokens][hidden]
  * the last hidden states and w [vocab][hidden] the head's weights (both bf16):
  *   z[t][v] = scale * sum_h x[t][h] w[v][h],  lse[t] = log sum_v exp z[t][v],  p = exp(z - lse).
+ * Logits may be as large or as low as binary32 holds (a part of the vocabulary masked by -1e10 or
+ * by the lowest finite value, say), and -inf.
  *
  * bsq_linear_ce -- softmax cross entropy: loss[t] = lse[t] - z[t][labels[t]], which is
  * minus the log-probability of the label.  labels [tokens] int32: a label outside
