@@ -320,6 +320,7 @@ __global__ __launch_bounds__(256) void k_lists(ListArgs a) {
 // different m still 64 or more apart.  (R is held as 2^-20 of it, which every finite m leaves in binary32 up to a scale of
 // 2^19.)  Logits of -1e10 and the lowest finite values, which mask parts of a vocabulary, are of this kind.
 constexpr float NOTHING = -3e38f, FAR = 1073741824.0f, KEY = 1.0f / (1 << 20), MOST = 3.40282347e38f;
+constexpr float LARGE = 65536.0f;  // of R, from where on roundings of the logits' size show in a sum
 __device__ __forceinline__ float2 merge(float2 a, float2 b) {
     const float r = max_num(a.x, b.x);
     auto scaled = [&](float2 x) { return ldexpf(x.y, (int)(max_num(x.x - r, -512.0f * KEY) * (1 / KEY))); };
@@ -495,6 +496,9 @@ __global__ __launch_bounds__(64 * Loop::WAVES, 1) void k_logits(HeadArgs a) {
             }
         }
     };
+    float k_[NQ];  // exponents of e are fmaf(acc, k_, -lse_)
+#pragma unroll
+    for (int j = 0; j < NQ; ++j) k_[j] = a.scale;
     // columns past the end (the last tile's)
     const int end = (int)vend - base;
     if (p0 + TP > vend) {
@@ -505,6 +509,27 @@ __global__ __launch_bounds__(64 * Loop::WAVES, 1) void k_logits(HeadArgs a) {
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
                     if (value(i, v) >= end) acc[i][j][v] = -INFINITY;  // (its exponential is 0)
+    }
+    if constexpr (BACK) {
+        // Where lse is large, z is rounded as the forward rounds the largest logit into it, whose p so is 1, and no p is more.
+        bool large = false;
+#pragma unroll
+        for (int j = 0; j < NQ; ++j) large |= !(fabsf(lse_[j]) <= LARGE / 2);
+        if (__builtin_expect(__ballot(large) != 0, 0)) {
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+                if (!(fabsf(lse_[j]) <= LARGE / 2)) {
+#pragma unroll
+                    for (int i = 0; i < NP; ++i)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) {
+                            const float d = a.scale * acc[i][j][v] - lse_[j];
+                            acc[i][j][v] = d > 0.0f && lse_[j] > -INFINITY ? 0.0f : d;
+                        }
+                    k_[j] = 1.0f;
+                    lse_[j] = 0.0f;
+                }
+        }
     }
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -542,7 +567,7 @@ __global__ __launch_bounds__(64 * Loop::WAVES, 1) void k_logits(HeadArgs a) {
             for (int i = 0; i < NP; ++i)
 #pragma unroll
                 for (int v = 0; v < 4; ++v)
-                    acc[i][j][v] = c_[j] * __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], a.scale, -lse_[j]) * LOG2E);
+                    acc[i][j][v] = c_[j] * __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], k_[j], -lse_[j]) * LOG2E);
             if (__ballot(d_[j] != 0.0f))
                 hits(j, [&](int64_t e) { return LIST ? a.sq[e] : 1.0f; }, [&](int at, float w) {
                     if (d_[j] == 0.0f) return;
@@ -634,7 +659,7 @@ __global__ __launch_bounds__(256) void k_finish(FinishArgs a) {
         }
         __syncthreads();
     }
-    constexpr float LN2 = 0.693147181f, LARGE = 65536.0f, HUGE_Z = 1e38f;
+    constexpr float LN2 = 0.693147181f, HUGE_Z = 1e38f;
     const float ln = logf(all.y);
     // lse of a pair's (key, ln s).  Beyond LARGE the roundings of kappa and of R ln 2 would show beside ln s: 64 bits, or the
     // largest logit as it is rounded by itself.

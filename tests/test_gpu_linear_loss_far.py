@@ -131,3 +131,54 @@ def test_far_rows(bsq_gpu, T, V, distill, value, sign):
         if distill:
             tol = tol + 2 * U * torch.where(tie, at.abs().clamp(max=65536.0), at.abs())
         assert (torch.isinf(got[0]) == inf).all() and ((got[0].double() - n).abs() <= tol)[~inf].all()
+
+
+@pytest.mark.parametrize("T,V", WIDTHS)
+@pytest.mark.parametrize("value", [1e5, 1e9, 1e10, 1e20, 1e30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_far_rows_backward(bsq_gpu, T, V, value, sign):
+    """One logit far above the others, all of them far from 0: its p is 1, the others' 0."""
+    b = bsq_gpu
+    H = 64
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[torch.arange(T), torch.arange(T) % 8] = 1.0
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    top = torch.tensor(sign * value, device="cuda").bfloat16().float()
+    w[:, :8] = (top * (0.5 if sign > 0 else 2.0)).bfloat16()
+    best = torch.randperm(V, generator=gen, device="cuda")[:8]
+    w[best, torch.arange(8)] = top.bfloat16()
+    best = best[torch.arange(T, device="cuda") % 8]
+    lab = torch.where(torch.arange(T, device="cuda") % 3 == 0, best, (best + 5) % V).int()
+    dloss = torch.rand(T, generator=gen, device="cuda") + 0.5
+    rows = torch.arange(T, device="cuda")
+    for scale in (1.0, 0.5, 0.8, 1.25):
+        lse = b.bsq_linear_ce(x, w, lab, scale=scale)[1]
+        g = torch.zeros(T, V, dtype=torch.float64, device="cuda")
+        g[rows, best] += scale * dloss.double()
+        g[rows, lab.long()] -= scale * dloss.double()
+        dx, dw = b.bsq_linear_ce_bwd(x, w, lab, lse, dloss=dloss, scale=scale, dx_dtype=b.BSQ_F32, dw_dtype=b.BSQ_F32)
+        # p is exactly 1 or 0, and g two products: a rounding each, and one for each of the sums' (T / 8 equal signs at most)
+        want = g.t() @ x.double()
+        assert ((dw.double() - want).abs() <= (8 + T / 32) * U * (g.abs().t() @ x.double())).all()
+        want = g @ w.double()
+        assert ((dx.double() - want).abs() <= 16 * U * (g.abs() @ w.double().abs())).all()
+
+
+@pytest.mark.parametrize("T", [20, 300])
+def test_p_is_at_most_one(bsq_gpu, T):
+    """Equal largest logits, so large that their number does not show in lse: each has a p from 0 to 1."""
+    b = bsq_gpu
+    V, H = 1000, 8
+    x = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1.0
+    w = torch.zeros(V, H, dtype=torch.bfloat16, device="cuda")
+    lab = torch.zeros(T, dtype=torch.int32, device="cuda")
+    for value in (1e6, -1e6, 1e9, -1e9, 1e20, -1e20):
+        for scale in (1.0, 0.7):
+            w[:, 0] = value
+            lse = b.bsq_linear_ce(x, w, lab, scale=scale)[1]
+            # with dlse alone, dw of column 0 is scale p, summed over the tokens
+            p = b.bsq_linear_ce_bwd(x, w, lab, lse, dlse=torch.ones(T, device="cuda"), scale=scale, flags=b.BSQ_WGRAD,
+                                    dw_dtype=b.BSQ_F32)[1][:, 0] / (scale * T)
+            assert (p >= 0).all() and (p <= 1 + (T / 32 + 40) * U).all()
