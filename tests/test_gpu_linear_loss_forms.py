@@ -157,3 +157,42 @@ def test_three_parts(bsq_gpu, name, K):
         for out, want, kind in zip(got, (g @ d.w.double(), g.t() @ x), kinds):
             if kind:
                 assert (out.double() - want).norm() <= THREE_PARTS * want.norm()
+
+
+@pytest.mark.parametrize("T,V,H", [(20, 900, 72), (100, 4001, 328), (1100, 1000, 72)])
+def test_graph_of_lists(bsq_gpu, T, V, H):
+    """Distillation's two passes captured together and replayed on other lists, with eager calls between; two graphs share
+    a workspace."""
+    b = bsq_gpu
+    cases = [Data(T, V, H, 6) for _ in range(2)]
+    cases[1].ids, cases[1].tl = cases[1].ids.flip(0).contiguous(), cases[1].tl.flip(0).contiguous()
+    cases[1].x = cases[1].x.flip(0).contiguous()
+    x, w, ids, tl, dloss = (t.clone() for t in (cases[0].x, cases[0].w, cases[0].ids, cases[0].tl, cases[0].dloss))
+    room = max(b.bsq_linear_loss_workspace_size(T, H, V, 6, flags) for flags in (0, 3))
+    ws = torch.empty(room, dtype=torch.uint8, device="cuda")
+
+    def step():
+        out = b.bsq_linear_distill(x, w, ids, tl, workspace=ws)
+        return (*out, *b.bsq_linear_distill_bwd(x, w, ids, tl, out[1], dloss=dloss, workspace=ws))
+
+    step()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    for i in (0, 1, 0, 1, 1):
+        c = cases[i]
+        for to, of in ((x, c.x), (ids, c.ids), (tl, c.tl)):
+            to.copy_(of)
+        dloss.mul_(1.5)
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        for g, out in graphs:
+            for t in out:
+                t.fill_(3.0)
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, e) for a, e in zip(out, want))
