@@ -182,3 +182,33 @@ def test_p_is_at_most_one(bsq_gpu, T):
             p = b.bsq_linear_ce_bwd(x, w, lab, lse, dlse=torch.ones(T, device="cuda"), scale=scale, flags=b.BSQ_WGRAD,
                                     dw_dtype=b.BSQ_F32)[1][:, 0] / (scale * T)
             assert (p >= 0).all() and (p <= 1 + (T / 32 + 40) * U).all()
+
+
+@pytest.mark.parametrize("T,V", WIDTHS)
+@pytest.mark.parametrize("power", [27, 28, 29, 30, 31, 33])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_neighbouring_far_logits(bsq_gpu, T, V, power, sign):
+    """Logits of 2^27 to 2^33 that differ in their last bits, whose exponents a whole number of 24 bits still holds or no longer
+    does: two products a logit, whose sum binary32 holds."""
+    b = bsq_gpu
+    gen = torch.Generator(device="cuda").manual_seed(power + V)
+    x = torch.zeros(T, 8, dtype=torch.bfloat16, device="cuda")
+    x[:, :2] = 1.0
+    w = torch.zeros(V, 8, dtype=torch.bfloat16, device="cuda")
+    w[:, 0] = sign * 2.0 ** power * (1 + T % 3 / 128)
+    w[:, 1] = torch.randint(0, 250, (V,), generator=gen, device="cuda") * 2.0 ** (power - 23)
+    z = w[:, 0].double() + w[:, 1].double()
+    assert torch.equal(z, f32(z))
+    lab = torch.randint(0, V, (T,), generator=gen, device="cuda").int()
+    for scale in (1.0, 0.5, 0.7, 0.8, 1.25):
+        s = torch.tensor(scale, dtype=torch.float32).double().item()  # (as the call gets it)
+        top = torch.logsumexp(s * (z - z.max()), 0)
+        want = top - s * (z - z.max())[lab.long()]
+        # the merge's roundings, and a few of the label's distance from the largest
+        tol = (64 + V / 1024) * U + 8 * U * want
+        ce, lse = b.bsq_linear_ce(x, w, lab, scale=scale)
+        assert ((ce.double() - want).abs() <= tol).all()
+        assert ((lse.double() - (s * z.max() + top)).abs() <= 4 * U * (s * z.max()).abs()).all()
+        kl, same, at = b.bsq_linear_distill(x, w, lab[:, None].contiguous(), torch.zeros(T, 1, device="cuda"), scale=scale)
+        assert ((kl.double() - want).abs() <= tol).all() and torch.equal(same, lse)
+        assert torch.equal(at[:, 0], (s * z[lab.long()]).float())
