@@ -585,7 +585,8 @@ size_t bsq_grouped_gemm_fp8b128_workspace_size(int32_t num_experts);
  * NULL: none) the gradients of loss and lse, Q = sum_k q (cross entropy: the label alone, q = 1):
  *   g[t][v] = scale ((dloss Q + dlse) p[t][v] - dloss sum_{k: id = v} q[t][k])
  *   BSQ_DGRAD: dx[t][h] = sum_v g[t][v] w[v][h];  BSQ_WGRAD: dw[v][h] = sum_t g[t][v] x[t][h].
- *   lse is the forward's; p has its rounding, 2^-24 |lse| relatively, and is at most 1.  Tokens without a target, and those whose dloss and dlse are
+ *   lse is the forward's; p has lse's roundings, 2^-23 |lse| relatively (beyond |lse| = 2^15 p is at
+ *   most 1, and equal largest logits may get that each).  Tokens without a target, and those whose dloss and dlse are
  *   both 0, get dx 0 and add nothing to dw.  The teacher's side gets no gradient.
  *   dx [tokens][ld_dx], dw [vocab][ld_dw] in their dtype.  For bf16 outputs g is rounded to
  *   bf16 for the two products (up to 256 tokens: to a pair of bf16), for f32 outputs it is
